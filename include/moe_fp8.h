@@ -25,6 +25,13 @@
  *   moe_token_map_aligned_rows, moe_token_map_aligned,
  *   moe_expand_cast_fp8_padded
  *
+ * Around and inside the MoE block (each from its formula, stated at the call):
+ *   moe_block_norm, moe_block_norm_backward: the norms after and before a
+ *   block with its gate and the residual scale, and their gradients;
+ *   moe_expert_matvec: a few rows per expert times its 4-bit weights;
+ *   moe_balance_loss, moe_balance_loss_backward: the router's balance loss,
+ *   per-expert counts and gradient over packed sequences.
+ *
  * Device-side checks of the inputs' preconditions, for debugging:
  *   moe_check_scores, moe_check_topk_idx, moe_check_pos,
  *   moe_check_activations, and of a single-launch dispatch's barrier:
@@ -410,6 +417,221 @@ moe_status moe_expand_cast(const uint16_t* x_bf16, int64_t num_tokens, int32_t h
 moe_status swiglu_cast(const uint16_t* gate_up_bf16, int64_t num_rows, int32_t inter,
                        const float* row_weights, float clamp_value, const moe_cast_format* format,
                        uint8_t* out, void* out_sf, hipStream_t stream);
+
+/* Element types of the calls below. */
+#define MOE_DTYPE_BF16 0
+#define MOE_DTYPE_F32 1
+#define MOE_DTYPE_E4M3 2
+
+/* How a block's output is gated before it joins the residual. */
+#define MOE_GATE_NONE 0
+#define MOE_GATE_CHANNEL 1 /* gate fp32 [hidden]: one value per channel */
+#define MOE_GATE_TOKEN 2   /* gate fp32 [num_tokens]: one value per token */
+
+#define MOE_BLOCK_NORM_MAX_HIDDEN 16384
+#define MOE_BLOCK_NORM_MAX_TOKENS 4194304
+
+/*
+ * moe_block_norm -- what stands between two blocks of the residual stream: the
+ * norm after a block, its gate, the scaled residual, and the norm before the
+ * next block, in one pass.
+ *
+ * For each token row, with r the residual and y the block's output:
+ *   u  = y * rsqrt(mean(y^2) + eps) * post_weight   (post_weight NULL: u = y)
+ *   r' = residual_scale * r + gate * u              (gate NULL: 1)
+ *   n  = r' * rsqrt(mean(r'^2) + eps) * pre_weight
+ * in fp32; r' and n are rounded once each (to nearest even), n from the
+ * unrounded r'.  The sum of a row's squares must stay finite in fp32.
+ *   y NULL        no block: r' = r and only n is computed (then post_weight,
+ *                 gate and res_out must be NULL and residual_scale 1).
+ *   normed NULL   no norm before the next block (then pre_weight and pre_rstd
+ *                 must be NULL).
+ *
+ * residual       residual_dtype [T, H], rows residual_stride elements apart.
+ * y              act_dtype [T, H], rows y_stride elements apart, or NULL.
+ * residual_dtype, act_dtype   MOE_DTYPE_BF16 or MOE_DTYPE_F32, each.
+ * num_tokens     0 <= T <= MOE_BLOCK_NORM_MAX_TOKENS (else MOE_ERR_UNSUPPORTED).
+ * hidden         H, 1 <= H <= MOE_BLOCK_NORM_MAX_HIDDEN (above:
+ *                MOE_ERR_UNSUPPORTED).  Strides >= H.
+ * post_weight    fp32 [H], or NULL.
+ * gate           fp32 [H] (MOE_GATE_CHANNEL), fp32 [T] (MOE_GATE_TOKEN), NULL
+ *                iff gate_mode is MOE_GATE_NONE.
+ * residual_scale any number but NaN.
+ * pre_weight     fp32 [H]; given iff normed is.
+ * eps            >= 0.
+ * res_out        r', residual_dtype [T, H] contiguous.  May be `residual`
+ *                itself where that is contiguous.
+ * normed         n, act_dtype [T, H] contiguous, or NULL.  May be `y` itself
+ *                where that is contiguous.
+ * post_rstd,     fp32 [T]: the two factors rsqrt(mean + eps), which the
+ * pre_rstd       backward pass reads, or NULL.
+ * Any alignment of the element type; 16-byte aligned rows with H a multiple of
+ * 8 run on 16-byte accesses.
+ */
+moe_status moe_block_norm(const void* residual, int64_t residual_stride, int32_t residual_dtype, const void* y,
+                          int64_t y_stride, int32_t act_dtype, int64_t num_tokens, int32_t hidden,
+                          const float* post_weight, const float* gate, int32_t gate_mode, float residual_scale,
+                          const float* pre_weight, float eps, void* res_out, void* normed, float* post_rstd,
+                          float* pre_rstd, hipStream_t stream);
+
+/* Bytes of device workspace moe_block_norm_backward needs (a multiple of 256;
+ * 0 for an invalid or unsupported shape and for T == 0). */
+size_t moe_block_norm_backward_workspace_bytes(int64_t num_tokens, int32_t hidden);
+
+/*
+ * moe_block_norm_backward -- the gradients of moe_block_norm.
+ *
+ * With xh = r' * pre_rstd, yh = y * post_rstd (post_weight NULL: yh = y),
+ * g = grad_normed * pre_weight:
+ *   D  = grad_res_out + pre_rstd * (g - xh * mean(g * xh))
+ *   grad_residual    = residual_scale * D
+ *   grad_pre_weight  = sum over tokens of grad_normed * xh
+ *   grad_gate        = sum of D * yh * post_weight over tokens (per channel)
+ *                      or over channels (per token)
+ *   du = gate * D;  g' = du * post_weight
+ *   grad_post_weight = sum over tokens of du * yh
+ *   grad_y           = post_rstd * (g' - yh * mean(g' * yh))   (post_weight
+ *                      NULL: du)
+ * in fp32.  The sums over tokens are added in a fixed order: the same inputs
+ * give the same bits.
+ *
+ * grad_res_out   residual_dtype [T, H] contiguous, or NULL for zero (then
+ *                grad_normed is required).
+ * grad_normed    act_dtype [T, H] contiguous; given iff pre_weight is.
+ * res_out        r' as the forward pass stored it, rows res_out_stride apart;
+ *                read iff pre_weight is given.
+ * y              the forward pass's y, rows y_stride apart, or NULL.
+ * post_weight, gate, gate_mode, residual_scale, pre_weight: as forward.
+ * post_rstd, pre_rstd   fp32 [T] from the forward pass; required with their
+ *                weights.
+ * grad_residual  residual_dtype [T, H] contiguous output.
+ * grad_y         act_dtype [T, H] contiguous output; given iff y is.
+ * grad_post_weight, grad_gate, grad_pre_weight   fp32 outputs of their
+ *                parameters' shapes; given iff the parameter is.
+ * workspace      >= moe_block_norm_backward_workspace_bytes(T, H) bytes,
+ *                256-byte aligned, if any of post_weight, a channel gate and
+ *                pre_weight is given; contents need not be initialised.
+ * With T == 0 the parameters' gradients are zeroed.
+ */
+moe_status moe_block_norm_backward(const void* grad_res_out, const void* grad_normed, const void* res_out,
+                                   int64_t res_out_stride, int32_t residual_dtype, const void* y, int64_t y_stride,
+                                   int32_t act_dtype, int64_t num_tokens, int32_t hidden, const float* post_weight,
+                                   const float* gate, int32_t gate_mode, float residual_scale,
+                                   const float* pre_weight, const float* post_rstd, const float* pre_rstd,
+                                   void* grad_residual, void* grad_y, float* grad_post_weight, float* grad_gate,
+                                   float* grad_pre_weight, void* workspace, size_t workspace_bytes,
+                                   hipStream_t stream);
+
+#define MOE_SCORE_SOFTMAX 0 /* p = softmax(logits) */
+#define MOE_SCORE_SIGMOID 1 /* p = sigmoid(logits) / sum of the row's sigmoids */
+#define MOE_BALANCE_MAX_SEQS 65536
+
+/* Bytes of device workspace moe_balance_loss needs (a multiple of 256).
+ * Returns 0 for an invalid shape. */
+size_t moe_balance_loss_workspace_bytes(int64_t num_tokens, int32_t num_experts, int32_t num_seqs);
+
+/*
+ * moe_balance_loss -- the router's balance loss of each packed sequence, with
+ * the copies each expert receives.
+ *
+ * With p[t, :] the normalised scores of token t, n_s the live tokens of
+ * sequence s and c[s, e] the copies (t, k) of its live tokens with
+ * topk_idx[t, k] == e:
+ *   prob_mean[s, e] = sum over the live tokens of p[t, e] / n_s
+ *   loss[s]         = E / (K n_s) * sum over e of c[s, e] * prob_mean[s, e]
+ * which is 1 for a perfectly even load; a sequence without live tokens gives
+ * loss, counts and means of 0.  All sums are fp32 or whole numbers, in a fixed
+ * order: the same inputs give the same bits.
+ *
+ * A row of nothing but -inf has p = 0 (it still counts in n_s).  A logit of
+ * -inf takes its expert out of the row; NaN or +inf (softmax) makes the row's
+ * p NaN.
+ *
+ * logits         logits_dtype [T, E], rows row_stride elements apart.
+ * logits_dtype   MOE_DTYPE_BF16 or MOE_DTYPE_F32.
+ * num_tokens     0 <= T <= (2^31 - 1) / 16.
+ * num_experts    E, 1 <= E <= 1024.
+ * score          MOE_SCORE_SOFTMAX or MOE_SCORE_SIGMOID.
+ * topk_idx       int64 [T, K] (from moe_topk_gate or any source); an id
+ *                outside [0, E) is not counted.
+ * num_topk       K, 1 <= K <= min(E, 16).
+ * token_mask     uint8 [T], 0 = not live (the token's logits and ids are not
+ *                read), or NULL.
+ * seq_offsets    int32 [S + 1], non-decreasing, within [0, T]: sequence s is
+ *                the tokens [seq_offsets[s], seq_offsets[s + 1]); tokens
+ *                outside all of them belong to none.  NULL: one sequence of
+ *                all tokens (S == 1).
+ * num_seqs       S, 1 <= S <= MOE_BALANCE_MAX_SEQS.
+ * loss           fp32 [S] output;  counts int32 [S, E] output;
+ * seq_tokens     int32 [S] output, n_s;  prob_mean fp32 [S, E] output or NULL.
+ * workspace      >= moe_balance_loss_workspace_bytes(T, E, S) bytes, 256-byte
+ *                aligned; contents need not be initialised.
+ */
+moe_status moe_balance_loss(const void* logits, int32_t logits_dtype, int64_t row_stride, int64_t num_tokens,
+                            int32_t num_experts, int32_t score, const int64_t* topk_idx, int32_t num_topk,
+                            const uint8_t* token_mask, const int32_t* seq_offsets, int32_t num_seqs, float* loss,
+                            int32_t* counts, int32_t* seq_tokens, float* prob_mean, void* workspace,
+                            size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * moe_balance_loss_backward -- the gradient of sum over s of grad_loss[s] *
+ * loss[s] with respect to the logits (the counts carry none):
+ *   a[s, e] = grad_loss[s] * E / (K n_s^2) * counts[s, e]
+ *   grad_logits[t, j] = p_j * (a[s, j] - sum over e of a[s, e] p_e)
+ *                       [* (1 - sigmoid(logits[t, j])) for MOE_SCORE_SIGMOID]
+ * A token that is masked or in no sequence gets 0, whatever its logits hold.
+ *
+ * grad_loss      fp32 [S].
+ * counts, seq_tokens   from moe_balance_loss.
+ * grad_logits    logits_dtype [T, E] contiguous output.
+ * The others as for moe_balance_loss.  T == 0 enqueues nothing.
+ */
+moe_status moe_balance_loss_backward(const float* grad_loss, const void* logits, int32_t logits_dtype,
+                                     int64_t row_stride, int64_t num_tokens, int32_t num_experts, int32_t score,
+                                     int32_t num_topk, const uint8_t* token_mask, const int32_t* seq_offsets,
+                                     int32_t num_seqs, const int32_t* counts, const int32_t* seq_tokens,
+                                     void* grad_logits, hipStream_t stream);
+
+#define MOE_MATVEC_MAX_WIDTH 1048576
+
+/*
+ * moe_expert_matvec -- the experts' products at decode: rows grouped by
+ * expert, a few per expert, times that expert's 4-bit weights.
+ *
+ *   out[r, n] = bf16( sum over k of x[r', k] * w[e, n, k] * sf[e, n, k / g] )
+ * for the rows r of expert e, expert_offsets[e] <= r < expert_offsets[e + 1],
+ * with r' = row_token[r] if given (the token rows themselves, without an
+ * expand) and r otherwise; products exact, sums fp32.  A row whose row_token
+ * is outside [0, x_rows) (the padding rows of an aligned map) gets zeros;
+ * rows of no expert are not written.  Weights are what moe_expand_cast writes
+ * for the weight matrix in the e2m1 format.  The time goes by the weights of
+ * the experts that have rows; any number of rows is right.
+ *
+ * x              MOE_DTYPE_BF16: bf16 [x_rows, inner].  MOE_DTYPE_E4M3: e4m3
+ *                codes [x_rows, inner] with one scale for each 128 channels,
+ *                as moe_expand_cast_fp8 and swiglu_cast_fp8 write them.
+ *                16-byte aligned.
+ * x_sf           fp32 [x_rows, inner / 128] (e4m3), else NULL.
+ * row_token      int32 [num_rows], or NULL (then x_rows == num_rows).
+ * num_rows       R >= 0.
+ * inner          a multiple of group_size, and of 128 for e4m3 rows.
+ * out_width      N >= 1.  inner, N <= MOE_MATVEC_MAX_WIDTH (above:
+ *                MOE_ERR_UNSUPPORTED).
+ * num_experts    E, 1 <= E <= 1024.
+ * expert_offsets int32 [E + 1], non-decreasing, within [0, R] (from
+ *                moe_token_map); NULL for E == 1: all rows.
+ * w_codes        e2m1 [E, N, inner / 2] bytes, code 2i in the low nibble of
+ *                byte i, 16-byte aligned.
+ * w_sf           [E, N, inner / group_size]: UE8M0 bytes (sf_ue8m0 = 1) or
+ *                fp32 (0).
+ * group_size     32 or 128 (anything else: MOE_ERR_UNSUPPORTED).
+ * out_bf16       bf16 [R, N] output.
+ */
+moe_status moe_expert_matvec(const void* x, int32_t x_dtype, const float* x_sf, int64_t x_rows,
+                             const int32_t* row_token, int64_t num_rows, int32_t inner, int32_t out_width,
+                             int32_t num_experts, const int32_t* expert_offsets, const uint8_t* w_codes,
+                             const void* w_sf, int32_t group_size, int32_t sf_ue8m0, uint16_t* out_bf16,
+                             hipStream_t stream);
 
 /* moe_route modes */
 #define MOE_ROUTE_AUTO 0  /* the local form up to 16 tokens; the fused form when the batch has more than

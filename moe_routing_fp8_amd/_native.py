@@ -61,6 +61,18 @@ _SIGNATURES = {
     "moe_dispatch_workspace_bytes": ([_i64, _i32, _i32], _sz),
     "moe_dispatch": ([_p, _p, _i64, _i32, _i32, _i32, _i32, _i32, _p, _p, _p, _p, _p, _p, _p, _p, _p, _p,
                       _sz, _i32, _p], ctypes.c_int),
+    "moe_block_norm": ([_p, _i64, _i32, _p, _i64, _i32, _i64, _i32, _p, _p, _i32, _f32, _p, _f32, _p, _p, _p, _p,
+                        _p], ctypes.c_int),
+    "moe_block_norm_backward_workspace_bytes": ([_i64, _i32], _sz),
+    "moe_block_norm_backward": ([_p, _p, _p, _i64, _i32, _p, _i64, _i32, _i64, _i32, _p, _p, _i32, _f32, _p, _p, _p,
+                                 _p, _p, _p, _p, _p, _p, _sz, _p], ctypes.c_int),
+    "moe_balance_loss_workspace_bytes": ([_i64, _i32, _i32], _sz),
+    "moe_balance_loss": ([_p, _i32, _i64, _i64, _i32, _i32, _p, _i32, _p, _p, _i32, _p, _p, _p, _p, _p, _sz, _p],
+                         ctypes.c_int),
+    "moe_balance_loss_backward": ([_p, _p, _i32, _i64, _i64, _i32, _i32, _i32, _p, _p, _i32, _p, _p, _p, _p],
+                                  ctypes.c_int),
+    "moe_expert_matvec": ([_p, _i32, _p, _i64, _p, _i64, _i32, _i32, _i32, _p, _p, _p, _i32, _i32, _p, _p],
+                          ctypes.c_int),
     "moe_check_scores": ([_p, _i64, _i32, _i32, _p, _p], ctypes.c_int),
     "moe_check_topk_idx": ([_p, _i64, _i32, _i32, _p, _p], ctypes.c_int),
     "moe_check_pos_workspace_bytes": ([_i64], _sz),
@@ -79,6 +91,17 @@ MOE_ROUTE_AUTO = 0
 MOE_ROUTE_FUSED = 1
 MOE_ROUTE_SPLIT = 2
 MOE_ROUTE_LOCAL = 3
+
+MOE_DTYPE_BF16 = 0
+MOE_DTYPE_F32 = 1
+MOE_DTYPE_E4M3 = 2
+
+MOE_GATE_NONE = 0
+MOE_GATE_CHANNEL = 1
+MOE_GATE_TOKEN = 2
+
+MOE_SCORE_SOFTMAX = 0
+MOE_SCORE_SIGMOID = 1
 
 MOE_DISPATCH_AUTO = 0
 MOE_DISPATCH_SINGLE_LAUNCH = 1
@@ -737,3 +760,291 @@ def swiglu_cast(gate_up: torch.Tensor, row_weights: Optional[torch.Tensor] = Non
     _call("swiglu_cast", dev, stream, _ptr(gate_up), R, inter, _ptr(row_weights), float(clamp_value),
           ctypes.byref(fmt), _ptr(o), _ptr(sf))
     return o, sf
+
+
+_NORM_DTYPES = {torch.bfloat16: MOE_DTYPE_BF16, torch.float32: MOE_DTYPE_F32}
+
+
+
+def _need_rows(t: torch.Tensor, name):
+    """A 2-d bf16 or fp32 device tensor with contiguous rows; returns the stride between rows in elements."""
+    if t.dtype not in _NORM_DTYPES or t.dim() != 2 or not t.is_cuda:
+        raise ValueError(f"{name}: expected a 2-d bf16 or fp32 device tensor, got {t.dtype} {tuple(t.shape)} on "
+                         f"{t.device}")
+    n, width = t.shape
+    if width > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name}: elements of a row must be adjacent, got strides {t.stride()}")
+    stride = t.stride(0) if n > 1 else max(width, 1)
+    if stride < width:
+        raise ValueError(f"{name}: rows overlap (strides {t.stride()})")
+    return stride
+
+
+def _need_param(t: Optional[torch.Tensor], n, name, dev):
+    """A parameter vector: contiguous fp32 [n] on `dev`, or None."""
+    if t is not None and (t.dtype != torch.float32 or t.shape != (n,) or t.device != dev or not t.is_contiguous()):
+        raise ValueError(f"{name}: expected a contiguous fp32 tensor of shape {(n,)} on {dev}, got {t.dtype} "
+                         f"{tuple(t.shape)} on {t.device}")
+
+
+def _gate_mode(gate: Optional[torch.Tensor], T, H, dev):
+    """The gate mode of a gate fp32 [H] (one value per channel) or [T, 1] (one per token)."""
+    if gate is None:
+        return MOE_GATE_NONE
+    if gate.dtype == torch.float32 and gate.device == dev and gate.is_contiguous():
+        if gate.shape == (H,):
+            return MOE_GATE_CHANNEL
+        if gate.shape == (T, 1):
+            return MOE_GATE_TOKEN
+    raise ValueError(f"gate: expected a contiguous fp32 tensor of shape {(H,)} (per channel) or {(T, 1)} (per token) "
+                     f"on {dev}, got {gate.dtype} {tuple(gate.shape)} on {gate.device}")
+
+
+def moe_block_norm(residual: torch.Tensor, y: Optional[torch.Tensor] = None,
+                   post_weight: Optional[torch.Tensor] = None, gate: Optional[torch.Tensor] = None,
+                   residual_scale: float = 1.0, pre_weight: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                   act_dtype: Optional[torch.dtype] = None, with_rstd: bool = False, out=None, stream=None):
+    """The norm after a block, its gate, the scaled residual and the norm before the next block, in one pass:
+    u = rmsnorm(y) * post_weight, r' = residual_scale * residual + gate * u, n = rmsnorm(r') * pre_weight.
+    residual [T, H] and y [T, H] (None: no block, r' = residual) are bf16 or fp32, each with any row stride;
+    gate fp32 [H] or [T, 1].  Returns (r', n, post_rstd, pre_rstd): r' in the residual's type (None without y), n in
+    y's (`act_dtype`, by default the residual's, without y; None without pre_weight), and with `with_rstd` the
+    fp32 [T] factors that the backward pass reads (else None).  `out`: these four; r' may be the residual
+    itself."""
+    rs = _need_rows(residual, "residual")
+    T, H = residual.shape
+    dev = residual.device
+    ys = H
+    if y is not None:
+        ys = _need_rows(y, "y")
+        _shape(y, (T, H), "y")
+        _device(residual, y)
+        if act_dtype is not None and act_dtype != y.dtype:
+            raise ValueError(f"act_dtype {act_dtype}: y is {y.dtype}")
+        act_dtype = y.dtype
+    elif act_dtype is None:
+        act_dtype = residual.dtype
+    if act_dtype not in _NORM_DTYPES:
+        raise ValueError(f"act_dtype: expected bf16 or fp32, got {act_dtype}")
+    _need_param(post_weight, H, "post_weight", dev)
+    _need_param(pre_weight, H, "pre_weight", dev)
+    mode = _gate_mode(gate, T, H, dev)
+    if y is None and (post_weight is not None or gate is not None or residual_scale != 1.0 or pre_weight is None):
+        raise ValueError("moe_block_norm: without y there is only the norm before the next block (pre_weight)")
+    if out is None:
+        with _alloc_on(stream):
+            out = (torch.empty((T, H), dtype=residual.dtype, device=dev) if y is not None else None,
+                   torch.empty((T, H), dtype=act_dtype, device=dev) if pre_weight is not None else None,
+                   torch.empty(T, device=dev) if with_rstd and post_weight is not None else None,
+                   torch.empty(T, device=dev) if with_rstd and pre_weight is not None else None)
+        res_out, normed, post_rstd, pre_rstd = out
+    else:
+        res_out, normed, post_rstd, pre_rstd = out
+        _need_out(res_out, residual.dtype, (T, H), "res_out", dev)
+        _need_out(normed, act_dtype, (T, H), "normed", dev)
+        _need_out(post_rstd, torch.float32, (T,), "post_rstd", dev)
+        _need_out(pre_rstd, torch.float32, (T,), "pre_rstd", dev)
+        if (res_out is None) != (y is None) or (normed is None) != (pre_weight is None):
+            raise ValueError("out: res_out goes with y and normed with pre_weight")
+    _call("moe_block_norm", dev, stream, _ptr(residual), rs, _NORM_DTYPES[residual.dtype], _ptr(y), ys,
+          _NORM_DTYPES[act_dtype], T, H, _ptr(post_weight), _ptr(gate), mode, float(residual_scale),
+          _ptr(pre_weight), float(eps), _ptr(res_out), _ptr(normed), _ptr(post_rstd), _ptr(pre_rstd))
+    return out
+
+
+def moe_block_norm_backward_workspace_bytes(num_tokens: int, hidden: int) -> int:
+    return int(lib().moe_block_norm_backward_workspace_bytes(num_tokens, hidden))
+
+
+def moe_block_norm_backward(grad_res_out: Optional[torch.Tensor], grad_normed: Optional[torch.Tensor],
+                            res_out: torch.Tensor, y: Optional[torch.Tensor] = None,
+                            post_weight: Optional[torch.Tensor] = None, gate: Optional[torch.Tensor] = None,
+                            residual_scale: float = 1.0, pre_weight: Optional[torch.Tensor] = None,
+                            post_rstd: Optional[torch.Tensor] = None, pre_rstd: Optional[torch.Tensor] = None,
+                            workspace: Optional[torch.Tensor] = None, out=None, stream=None):
+    """The gradients of moe_block_norm, from those of its outputs (grad_res_out None: zero), its saved r' (`res_out`;
+    the residual itself without y), y and rstds.  Returns a dict of grad_residual, grad_y, grad_post_weight,
+    grad_gate and grad_pre_weight (None for what the forward pass was not given); `out`: such a dict."""
+    rs = _need_rows(res_out, "res_out")
+    T, H = res_out.shape
+    dev = res_out.device
+    ys = H
+    act_dtype = res_out.dtype if grad_normed is None else grad_normed.dtype
+    if y is not None:
+        ys = _need_rows(y, "y")
+        _shape(y, (T, H), "y")
+        _device(res_out, y)
+        act_dtype = y.dtype
+    if act_dtype not in _NORM_DTYPES:
+        raise ValueError(f"grad_normed: expected bf16 or fp32, got {act_dtype}")
+    _need_out(grad_res_out, res_out.dtype, (T, H), "grad_res_out", dev)
+    _need_out(grad_normed, act_dtype, (T, H), "grad_normed", dev)
+    _need_param(post_weight, H, "post_weight", dev)
+    _need_param(pre_weight, H, "pre_weight", dev)
+    _need_param(post_rstd, T, "post_rstd", dev)
+    _need_param(pre_rstd, T, "pre_rstd", dev)
+    mode = _gate_mode(gate, T, H, dev)
+    if (grad_normed is None) != (pre_weight is None) or (pre_weight is not None and pre_rstd is None):
+        raise ValueError("moe_block_norm_backward: pre_weight goes with grad_normed and pre_rstd")
+    if grad_res_out is None and grad_normed is None:
+        raise ValueError("moe_block_norm_backward: no gradient given")
+    if post_weight is not None and post_rstd is None:
+        raise ValueError("moe_block_norm_backward: post_weight goes with post_rstd")
+    if y is None and (post_weight is not None or gate is not None or residual_scale != 1.0):
+        raise ValueError("moe_block_norm_backward: without y there is only the norm before the next block")
+    if out is None:
+        with _alloc_on(stream):
+            out = {"grad_residual": torch.empty((T, H), dtype=res_out.dtype, device=dev),
+                   "grad_y": torch.empty((T, H), dtype=act_dtype, device=dev) if y is not None else None,
+                   "grad_post_weight": torch.empty(H, device=dev) if post_weight is not None else None,
+                   "grad_gate": torch.empty(gate.shape, device=dev) if gate is not None else None,
+                   "grad_pre_weight": torch.empty(H, device=dev) if pre_weight is not None else None}
+    else:
+        for key, dtype, shape, src in (("grad_residual", res_out.dtype, (T, H), res_out),
+                                       ("grad_y", act_dtype, (T, H), y),
+                                       ("grad_post_weight", torch.float32, (H,), post_weight),
+                                       ("grad_gate", torch.float32, None if gate is None else tuple(gate.shape), gate),
+                                       ("grad_pre_weight", torch.float32, (H,), pre_weight)):
+            if (out.get(key) is None) != (src is None):
+                raise ValueError(f"out: {key} goes with its input")
+            _need_out(out.get(key), dtype, shape, key, dev)
+    if workspace is None:
+        with _alloc_on(stream):
+            workspace = torch.empty(max(moe_block_norm_backward_workspace_bytes(T, H), 256), dtype=torch.uint8,
+                                    device=dev)
+    _call("moe_block_norm_backward", dev, stream, _ptr(grad_res_out), _ptr(grad_normed), _ptr(res_out), rs,
+          _NORM_DTYPES[res_out.dtype], _ptr(y), ys, _NORM_DTYPES[act_dtype], T, H, _ptr(post_weight), _ptr(gate), mode,
+          float(residual_scale), _ptr(pre_weight), _ptr(post_rstd), _ptr(pre_rstd), _ptr(out["grad_residual"]),
+          _ptr(out.get("grad_y")), _ptr(out.get("grad_post_weight")), _ptr(out.get("grad_gate")),
+          _ptr(out.get("grad_pre_weight")), _ptr(workspace), _workspace(workspace, dev))
+    return out
+
+
+_SCORES = {"softmax": MOE_SCORE_SOFTMAX, "sigmoid": MOE_SCORE_SIGMOID}
+
+
+def _balance_inputs(logits, score, token_mask, seq_offsets):
+    """What both directions of the balance loss check; returns (row stride, score, sequences)."""
+    stride = _need_rows(logits, "logits")
+    if score not in _SCORES:
+        raise ValueError(f"score: expected one of {sorted(_SCORES)}, got {score!r}")
+    if token_mask is not None:
+        if token_mask.dtype not in (torch.bool, torch.uint8) or not token_mask.is_contiguous():
+            raise ValueError(f"token_mask: expected a contiguous bool or uint8 tensor, got {token_mask.dtype}")
+        _shape(token_mask, (logits.shape[0],), "token_mask")
+    seqs = 1
+    if seq_offsets is not None:
+        _need(seq_offsets, torch.int32, 1, "seq_offsets")
+        seqs = seq_offsets.shape[0] - 1
+        if seqs < 1:
+            raise ValueError("seq_offsets: expected at least two entries")
+    _device(logits, token_mask, seq_offsets)
+    return stride, _SCORES[score], seqs
+
+
+def moe_balance_loss_workspace_bytes(num_tokens: int, num_experts: int, num_seqs: int = 1) -> int:
+    return int(lib().moe_balance_loss_workspace_bytes(num_tokens, num_experts, num_seqs))
+
+
+def moe_balance_loss(logits: torch.Tensor, topk_idx: torch.Tensor, score: str = "softmax",
+                     token_mask: Optional[torch.Tensor] = None, seq_offsets: Optional[torch.Tensor] = None,
+                     workspace: Optional[torch.Tensor] = None, out=None, stream=None):
+    """The balance loss of each packed sequence: logits bf16 or fp32 [T, E] (any row stride), topk_idx int64 [T, K],
+    token_mask bool [T] (False: not live), seq_offsets int32 [S+1] (None: one sequence) -> dict of loss fp32 [S],
+    counts int32 [S, E], seq_tokens int32 [S] (live tokens) and prob_mean fp32 [S, E].  `score`: "softmax", or
+    "sigmoid" divided by the row's sum."""
+    stride, mode, S = _balance_inputs(logits, score, token_mask, seq_offsets)
+    T, E = logits.shape
+    _need(topk_idx, torch.int64, 2, "topk_idx")
+    K = topk_idx.shape[1]
+    _shape(topk_idx, (T, K), "topk_idx")
+    dev = _device(logits, topk_idx)
+    if out is None:
+        with _alloc_on(stream):
+            out = {"loss": torch.empty(S, device=dev), "counts": torch.empty((S, E), dtype=torch.int32, device=dev),
+                   "seq_tokens": torch.empty(S, dtype=torch.int32, device=dev),
+                   "prob_mean": torch.empty((S, E), device=dev)}
+    else:
+        for key, dtype, shape in (("loss", torch.float32, (S,)), ("counts", torch.int32, (S, E)),
+                                  ("seq_tokens", torch.int32, (S,)), ("prob_mean", torch.float32, (S, E))):
+            _need_out(out.get(key), dtype, shape, key, dev)
+    if workspace is None:
+        with _alloc_on(stream):
+            workspace = torch.empty(max(moe_balance_loss_workspace_bytes(T, E, S), 256), dtype=torch.uint8, device=dev)
+    _call("moe_balance_loss", dev, stream, _ptr(logits), _NORM_DTYPES[logits.dtype], stride, T, E, mode,
+          _ptr(topk_idx), K, _ptr(token_mask), _ptr(seq_offsets), S, _ptr(out["loss"]), _ptr(out["counts"]),
+          _ptr(out["seq_tokens"]), _ptr(out.get("prob_mean")), _ptr(workspace), _workspace(workspace, dev))
+    return out
+
+
+def moe_balance_loss_backward(grad_loss: torch.Tensor, logits: torch.Tensor, counts: torch.Tensor,
+                              seq_tokens: torch.Tensor, num_topk: int, score: str = "softmax",
+                              token_mask: Optional[torch.Tensor] = None, seq_offsets: Optional[torch.Tensor] = None,
+                              out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """The gradient of sum_s grad_loss[s] * loss[s] with respect to the logits, in their type [T, E], from the
+    counts and seq_tokens of moe_balance_loss.  Tokens that are masked or in no sequence get 0."""
+    stride, mode, S = _balance_inputs(logits, score, token_mask, seq_offsets)
+    T, E = logits.shape
+    dev = logits.device
+    _need_out(grad_loss, torch.float32, (S,), "grad_loss", dev)
+    _need_out(counts, torch.int32, (S, E), "counts", dev)
+    _need_out(seq_tokens, torch.int32, (S,), "seq_tokens", dev)
+    if out is None:
+        with _alloc_on(stream):
+            out = torch.empty((T, E), dtype=logits.dtype, device=dev)
+    else:
+        _need_out(out, logits.dtype, (T, E), "out", dev)
+    _call("moe_balance_loss_backward", dev, stream, _ptr(grad_loss), _ptr(logits), _NORM_DTYPES[logits.dtype], stride,
+          T, E, mode, num_topk, _ptr(token_mask), _ptr(seq_offsets), S, _ptr(counts), _ptr(seq_tokens), _ptr(out))
+    return out
+
+
+def moe_expert_matvec(x: torch.Tensor, w_codes: torch.Tensor, w_sf: torch.Tensor,
+                      x_sf: Optional[torch.Tensor] = None, expert_offsets: Optional[torch.Tensor] = None,
+                      row_token: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                      stream=None) -> torch.Tensor:
+    """Rows grouped by expert times 4-bit weights: x bf16 [X, K], or e4m3 codes [X, K] with x_sf fp32 [X, K/128];
+    w_codes uint8 [E, N, K/2] (e2m1, as moe_expand_cast writes them; [N, K/2] for one matrix), w_sf uint8 (UE8M0) or
+    fp32 [E, N, K/g] with g = 32 or 128; expert_offsets int32 [E+1] (None: one matrix, all rows); row_token int32
+    [R] to read row r from x[row_token[r]] (None: R == X) -> bf16 [R, N].  Rows of no expert are not written."""
+    if x.dtype != torch.bfloat16 and x.dtype not in _FP8:
+        raise ValueError(f"x: expected bf16 or e4m3 codes, got {x.dtype}")
+    _need(x, x.dtype, 2, "x")
+    if w_codes.dim() == 2:
+        w_codes, w_sf = w_codes.unsqueeze(0), w_sf.unsqueeze(0)
+    _need(w_codes, torch.uint8, 3, "w_codes")
+    X, K = x.shape
+    E, N = w_codes.shape[:2]
+    _shape(w_codes, (E, N, K // 2), "w_codes")
+    ue8m0 = w_sf.dtype == torch.uint8
+    _need(w_sf, torch.uint8 if ue8m0 else torch.float32, 3, "w_sf")
+    G = w_sf.shape[2]
+    _shape(w_sf, (E, N, G), "w_sf")
+    if G == 0 or K % G != 0:
+        raise ValueError(f"w_sf: {G} scales for a row of {K} weights")
+    e4m3 = x.dtype != torch.bfloat16
+    if e4m3 != (x_sf is not None):
+        raise ValueError("x_sf: given with e4m3 rows, and only then")
+    if x_sf is not None:
+        _need(x_sf, torch.float32, 2, "x_sf")
+        _shape(x_sf, (X, K // 128), "x_sf")
+    if expert_offsets is not None:
+        _need(expert_offsets, torch.int32, 1, "expert_offsets")
+        _shape(expert_offsets, (E + 1,), "expert_offsets")
+    elif E != 1:
+        raise ValueError("expert_offsets: required with more than one expert")
+    R = X
+    if row_token is not None:
+        _need(row_token, torch.int32, 1, "row_token")
+        R = row_token.shape[0]
+    dev = _device(x, w_codes, w_sf, x_sf, expert_offsets, row_token)
+    if out is None:
+        with _alloc_on(stream):
+            out = torch.empty((R, N), dtype=torch.bfloat16, device=dev)
+    else:
+        _need_out(out, torch.bfloat16, (R, N), "out", dev)
+    if debug_enabled() and not e4m3:
+        _debug_raise("moe_expert_matvec", lambda: moe_check_activations(x, stream=stream), stream)
+    _call("moe_expert_matvec", dev, stream, _ptr(x), MOE_DTYPE_E4M3 if e4m3 else MOE_DTYPE_BF16, _ptr(x_sf), X,
+          _ptr(row_token), R, K, N, E, _ptr(expert_offsets), _ptr(w_codes), _ptr(w_sf), K // G, int(ue8m0), _ptr(out))
+    return out

@@ -1,0 +1,512 @@
+// The norms after and before a block of the residual stream, fused with the
+// block's gate and the residual scale, and their gradients.
+//
+// For a row of the residual r and of the block's output y (both H wide):
+//   u  = y * rsqrt(mean(y^2) + eps) * post_weight     (no post_weight: u = y)
+//   r' = residual_scale * r + gate * u                (no y: r' = r)
+//   n  = r' * rsqrt(mean(r'^2) + eps) * pre_weight
+// n is taken from r' in fp32, before r' is rounded for storage.
+//
+// One pass: a row is held in registers by one wave (short rows) or one
+// workgroup, so y and r are read once and r' and n written once; the two sums
+// of squares are the only exchanges between lanes.  The backward pass holds
+// the four arrays of a row the same way.  Its parameter gradients are sums
+// over rows: a workgroup walks over rows with a stride, keeps its columns'
+// running sums in registers, and writes them once; a second launch adds the
+// workgroups' sums in order.
+#include <hip/hip_runtime.h>
+
+#include "api_common.hpp"
+#include "math_device.hpp"
+#include "moe_fp8.h"
+
+namespace moe {
+namespace {
+
+constexpr int kMaxRowThreads = 1024;
+constexpr int kMaxHidden = MOE_BLOCK_NORM_MAX_HIDDEN;
+// Workgroups of the backward pass: two for each of the 256 compute units.
+constexpr int64_t kGradBlocks = 512;
+
+// 1 / sqrt(v): the hardware's estimate and one Newton step, which brings it
+// to within 1 ulp (0 and infinity keep the estimate's value).
+__device__ __forceinline__ float rsqrt_f32(float v) {
+    const float r = __builtin_amdgcn_rsqf(v);
+    const float e = __builtin_fmaf(-v * r, r, 1.0f);
+    const float n = __builtin_fmaf(0.5f * r, e, r);
+    return v > 0.0f && v < INFINITY ? n : r;
+}
+
+// Sum over the workgroup, in a fixed order; every thread receives it.
+// `part` holds one float per wave; the caller alternates between two of them
+// so that one barrier per sum is enough.
+__device__ __forceinline__ float block_sum(float v, float* part) {
+    v = wave_sum_f32(v);
+    const int waves = blockDim.x / kWave;
+    if (waves == 1) return v;
+    if ((threadIdx.x & (kWave - 1)) == 0) part[threadIdx.x / kWave] = v;
+    __syncthreads();
+    float s = 0.0f;
+    for (int w = 0; w < waves; ++w) s += part[w];
+    return s;
+}
+
+struct NormArgs {
+    const void* residual;
+    int64_t residual_stride;
+    const void* y;
+    int64_t y_stride;
+    int64_t num_tokens;
+    int hidden;
+    const float* post_weight;
+    const float* gate;
+    int gate_mode;
+    float residual_scale;
+    const float* pre_weight;
+    float eps;
+    void* res_out;
+    void* normed;
+    float* post_rstd;
+    float* pre_rstd;
+};
+
+// Thread i's j-th vector of a row starts at element (i + j * blockDim.x) * VEC.
+// VEC == 8 needs 16-byte aligned rows and H % 8 == 0; VEC == 1 takes any.
+template <typename TR, typename TA, int VEC, int VPT>
+__global__ __launch_bounds__(kMaxRowThreads) void block_norm_kernel(NormArgs a) {
+    __shared__ float part[2][kMaxRowThreads / kWave];
+    const int64_t t = blockIdx.x;
+    const int H = a.hidden;
+    const float inv_h = 1.0f / static_cast<float>(H);
+    float r[VPT][VEC], u[VPT][VEC];
+    float sq = 0.0f;
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+        const int e = (threadIdx.x + j * blockDim.x) * VEC;
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) r[j][i] = u[j][i] = 0.0f;
+        if (e < H) {
+            TR::template load<VEC>(a.residual, t * a.residual_stride + e, r[j]);
+            if (a.y != nullptr) TA::template load<VEC>(a.y, t * a.y_stride + e, u[j]);
+        }
+    }
+    if (a.y != nullptr) {
+        float rstd = 1.0f;
+        if (a.post_weight != nullptr) {
+#pragma unroll
+            for (int j = 0; j < VPT; ++j)
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) sq += u[j][i] * u[j][i];
+            rstd = rsqrt_f32(block_sum(sq, part[0]) * inv_h + a.eps);
+            if (threadIdx.x == 0 && a.post_rstd != nullptr) a.post_rstd[t] = rstd;
+        }
+        const float token_gate = a.gate_mode == MOE_GATE_TOKEN ? a.gate[t] : 1.0f;
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+            const int e = (threadIdx.x + j * blockDim.x) * VEC;
+            if (e >= H) continue;
+            float w[VEC], g[VEC];
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) {
+                w[i] = 1.0f;
+                g[i] = token_gate;
+            }
+            if (a.post_weight != nullptr) F32::load<VEC>(a.post_weight, e, w);
+            if (a.gate_mode == MOE_GATE_CHANNEL) F32::load<VEC>(a.gate, e, g);
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) r[j][i] = a.residual_scale * r[j][i] + g[i] * (u[j][i] * rstd * w[i]);
+            TR::template store<VEC>(a.res_out, t * H + e, r[j]);
+        }
+    }
+    if (a.normed == nullptr) return;
+    sq = 0.0f;
+#pragma unroll
+    for (int j = 0; j < VPT; ++j)
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) sq += r[j][i] * r[j][i];
+    const float rstd = rsqrt_f32(block_sum(sq, part[1]) * inv_h + a.eps);
+    if (threadIdx.x == 0 && a.pre_rstd != nullptr) a.pre_rstd[t] = rstd;
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+        const int e = (threadIdx.x + j * blockDim.x) * VEC;
+        if (e >= H) continue;
+        float w[VEC];
+        F32::load<VEC>(a.pre_weight, e, w);
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) w[i] = r[j][i] * rstd * w[i];
+        TA::template store<VEC>(a.normed, t * H + e, w);
+    }
+}
+
+struct NormGradArgs {
+    const void* grad_res_out;  // or nullptr: zero
+    const void* grad_normed;   // or nullptr: no norm before the next block
+    const void* res_out;
+    int64_t res_out_stride;
+    const void* y;
+    int64_t y_stride;
+    int64_t num_tokens;
+    int hidden;
+    const float* post_weight;
+    const float* gate;
+    int gate_mode;
+    float residual_scale;
+    const float* pre_weight;
+    const float* post_rstd;
+    const float* pre_rstd;
+    void* grad_residual;
+    void* grad_y;
+    float* grad_token_gate;
+    float* partials;  // [workgroup][parameter][H], parameters: post weight, channel gate, pre weight (those given)
+    int num_params;
+};
+
+template <typename TR, typename TA, int VEC, int VPT>
+__global__ __launch_bounds__(kMaxRowThreads) void block_norm_grad_kernel(NormGradArgs a) {
+    __shared__ float part[3][kMaxRowThreads / kWave];
+    const int H = a.hidden;
+    const float inv_h = 1.0f / static_cast<float>(H);
+    const bool pre = a.grad_normed != nullptr, block = a.y != nullptr, post = a.post_weight != nullptr;
+    const bool channel = a.gate_mode == MOE_GATE_CHANNEL;
+    float sum_post[VPT][VEC], sum_gate[VPT][VEC], sum_pre[VPT][VEC];
+#pragma unroll
+    for (int j = 0; j < VPT; ++j)
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) sum_post[j][i] = sum_gate[j][i] = sum_pre[j][i] = 0.0f;
+    for (int64_t t = blockIdx.x; t < a.num_tokens; t += gridDim.x) {
+        float d[VPT][VEC], yh[VPT][VEC];
+        float dot = 0.0f;
+        // D = dr' + rstd * (g - xh * mean(g * xh)), g = dn * pre_weight
+        {
+            float xh[VPT][VEC], g[VPT][VEC];
+            const float rstd = pre ? a.pre_rstd[t] : 0.0f;
+#pragma unroll
+            for (int j = 0; j < VPT; ++j) {
+                const int e = (threadIdx.x + j * blockDim.x) * VEC;
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) d[j][i] = yh[j][i] = xh[j][i] = g[j][i] = 0.0f;
+                if (e >= H) continue;
+                if (a.grad_res_out != nullptr) TR::template load<VEC>(a.grad_res_out, t * H + e, d[j]);
+                if (block) TA::template load<VEC>(a.y, t * a.y_stride + e, yh[j]);
+                if (pre) {
+                    float w[VEC];
+                    TR::template load<VEC>(a.res_out, t * a.res_out_stride + e, xh[j]);
+                    TA::template load<VEC>(a.grad_normed, t * H + e, g[j]);
+                    F32::load<VEC>(a.pre_weight, e, w);
+#pragma unroll
+                    for (int i = 0; i < VEC; ++i) {
+                        xh[j][i] *= rstd;
+                        sum_pre[j][i] += g[j][i] * xh[j][i];
+                        g[j][i] *= w[i];
+                        dot += g[j][i] * xh[j][i];
+                    }
+                }
+            }
+            if (pre) {
+                const float mean = block_sum(dot, part[0]) * inv_h;
+#pragma unroll
+                for (int j = 0; j < VPT; ++j)
+#pragma unroll
+                    for (int i = 0; i < VEC; ++i) d[j][i] += rstd * (g[j][i] - xh[j][i] * mean);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+            const int e = (threadIdx.x + j * blockDim.x) * VEC;
+            if (e >= H) continue;
+            float o[VEC];
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) o[i] = a.residual_scale * d[j][i];
+            TR::template store<VEC>(a.grad_residual, t * H + e, o);
+        }
+        if (block) {
+            const float rstd = post ? a.post_rstd[t] : 1.0f;
+            const float token_gate = a.gate_mode == MOE_GATE_TOKEN ? a.gate[t] : 1.0f;
+            float dot_gate = 0.0f;
+            dot = 0.0f;
+#pragma unroll
+            for (int j = 0; j < VPT; ++j) {
+                const int e = (threadIdx.x + j * blockDim.x) * VEC;
+                if (e >= H) continue;
+                float w[VEC], g[VEC];
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) {
+                    w[i] = 1.0f;
+                    g[i] = token_gate;
+                }
+                if (post) F32::load<VEC>(a.post_weight, e, w);
+                if (channel) F32::load<VEC>(a.gate, e, g);
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) {
+                    yh[j][i] *= rstd;
+                    const float along = d[j][i] * (yh[j][i] * w[i]);
+                    dot_gate += along;
+                    sum_gate[j][i] += along;
+                    d[j][i] *= g[i];                      // du
+                    sum_post[j][i] += d[j][i] * yh[j][i];
+                    d[j][i] *= w[i];
+                    dot += d[j][i] * yh[j][i];
+                }
+            }
+            if (a.gate_mode == MOE_GATE_TOKEN) {
+                dot_gate = block_sum(dot_gate, part[1]);
+                if (threadIdx.x == 0) a.grad_token_gate[t] = dot_gate;
+            }
+            if (post) {
+                const float mean = block_sum(dot, part[2]) * inv_h;
+#pragma unroll
+                for (int j = 0; j < VPT; ++j)
+#pragma unroll
+                    for (int i = 0; i < VEC; ++i) d[j][i] = rstd * (d[j][i] - yh[j][i] * mean);
+            }
+#pragma unroll
+            for (int j = 0; j < VPT; ++j) {
+                const int e = (threadIdx.x + j * blockDim.x) * VEC;
+                if (e < H) TA::template store<VEC>(a.grad_y, t * H + e, d[j]);
+            }
+        }
+        __syncthreads();  // the sums' exchange is written again by the next row
+    }
+    float* out = a.partials + static_cast<int64_t>(blockIdx.x) * a.num_params * H;
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+        const int e = (threadIdx.x + j * blockDim.x) * VEC;
+        if (e >= H) continue;
+        int64_t at = e;
+        if (post) {
+            F32::store<VEC>(out, at, sum_post[j]);
+            at += H;
+        }
+        if (channel) {
+            F32::store<VEC>(out, at, sum_gate[j]);
+            at += H;
+        }
+        if (pre) F32::store<VEC>(out, at, sum_pre[j]);
+    }
+}
+
+// The parameters' gradients: column sums of the workgroups' partials, rows in
+// order within each of kSumWaves waves, then the waves in order.
+constexpr int kSumWaves = 8;
+__global__ __launch_bounds__(kSumWaves* kWave) void block_norm_param_kernel(const float* __restrict__ partials,
+                                                                             int64_t blocks, int width, int H,
+                                                                             float* o0, float* o1, float* o2) {
+    __shared__ float lds[kSumWaves][kWave];
+    const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
+    const int c = blockIdx.x * kWave + lane;
+    float v = 0.0f;
+    if (c < width)
+        for (int64_t b = wave; b < blocks; b += kSumWaves) v += partials[b * width + c];
+    lds[wave][lane] = v;
+    __syncthreads();
+    if (wave == 0 && c < width) {
+        float s = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kSumWaves; ++w) s += lds[w][lane];
+        float* const outs[3] = {o0, o1, o2};
+        int left = c;
+        for (int k = 0; k < 3; ++k) {
+            if (outs[k] == nullptr) continue;
+            if (left < H) {
+                outs[k][left] = s;
+                break;
+            }
+            left -= H;
+        }
+    }
+}
+
+// Threads of a row: enough that VPT vectors of VEC each cover it, in whole waves.
+int row_threads(int H, int vec, int vpt) {
+    const int n = (H + vec * vpt - 1) / (vec * vpt);
+    return (n + kWave - 1) / kWave * kWave;
+}
+
+template <typename TR, typename TA, int VEC, int VPT>
+hipError_t launch_norm(const NormArgs& a, hipStream_t stream) {
+    hipLaunchKernelGGL((block_norm_kernel<TR, TA, VEC, VPT>), dim3(static_cast<unsigned>(a.num_tokens)),
+                       dim3(row_threads(a.hidden, VEC, VPT)), 0, stream, a);
+    return hipGetLastError();
+}
+template <typename TR, typename TA>
+hipError_t launch_norm_types(const NormArgs& a, bool vec, hipStream_t stream) {
+    if (vec) return a.hidden <= 8 * kMaxRowThreads ? launch_norm<TR, TA, 8, 1>(a, stream) : launch_norm<TR, TA, 8, 2>(a, stream);
+    return a.hidden <= 4 * kMaxRowThreads ? launch_norm<TR, TA, 1, 4>(a, stream) : launch_norm<TR, TA, 1, 16>(a, stream);
+}
+
+template <typename TR, typename TA, int VEC, int VPT>
+hipError_t launch_grad(const NormGradArgs& a, int64_t blocks, hipStream_t stream) {
+    hipLaunchKernelGGL((block_norm_grad_kernel<TR, TA, VEC, VPT>), dim3(static_cast<unsigned>(blocks)),
+                       dim3(row_threads(a.hidden, VEC, VPT)), 0, stream, a);
+    return hipGetLastError();
+}
+template <typename TR, typename TA>
+hipError_t launch_grad_types(const NormGradArgs& a, int64_t blocks, bool vec, hipStream_t stream) {
+    if (vec)
+        return a.hidden <= 8 * kMaxRowThreads ? launch_grad<TR, TA, 8, 1>(a, blocks, stream)
+                                              : launch_grad<TR, TA, 8, 2>(a, blocks, stream);
+    return a.hidden <= 4 * kMaxRowThreads ? launch_grad<TR, TA, 1, 4>(a, blocks, stream)
+                                          : launch_grad<TR, TA, 1, 16>(a, blocks, stream);
+}
+
+// Calls f with the two element types.
+template <typename F>
+hipError_t with_types(int res, int act, F&& f) {
+    if (res == MOE_DTYPE_BF16) return act == MOE_DTYPE_BF16 ? f(Bf16{}, Bf16{}) : f(Bf16{}, F32{});
+    return act == MOE_DTYPE_BF16 ? f(F32{}, Bf16{}) : f(F32{}, F32{});
+}
+
+bool dtype_ok(int32_t d) { return d == MOE_DTYPE_BF16 || d == MOE_DTYPE_F32; }
+int dtype_bytes(int32_t d) { return d == MOE_DTYPE_BF16 ? 2 : 4; }
+// Rows of 8-element vectors: 16-byte aligned start and stride (a null pointer passes).
+bool vec_rows(const void* p, int64_t stride, int32_t dtype) {
+    return aligned(p, 16) && stride * dtype_bytes(dtype) % 16 == 0;
+}
+
+int64_t grad_blocks(int64_t T) { return T < kGradBlocks ? T : kGradBlocks; }
+
+}  // namespace
+}  // namespace moe
+
+extern "C" {
+
+moe_status moe_block_norm(const void* residual, int64_t residual_stride, int32_t residual_dtype, const void* y,
+                          int64_t y_stride, int32_t act_dtype, int64_t num_tokens, int32_t hidden,
+                          const float* post_weight, const float* gate, int32_t gate_mode, float residual_scale,
+                          const float* pre_weight, float eps, void* res_out, void* normed, float* post_rstd,
+                          float* pre_rstd, hipStream_t stream) {
+    using namespace moe;
+    if (num_tokens < 0 || hidden < 1 || !dtype_ok(residual_dtype) || !dtype_ok(act_dtype))
+        return MOE_ERR_INVALID_ARGUMENT;
+    if (gate_mode != MOE_GATE_NONE && gate_mode != MOE_GATE_CHANNEL && gate_mode != MOE_GATE_TOKEN)
+        return MOE_ERR_INVALID_ARGUMENT;
+    if (!(eps >= 0.0f) || residual_scale != residual_scale) return MOE_ERR_INVALID_ARGUMENT;
+    if ((gate_mode != MOE_GATE_NONE) != (gate != nullptr)) return MOE_ERR_INVALID_ARGUMENT;
+    if (post_rstd != nullptr && post_weight == nullptr) return MOE_ERR_INVALID_ARGUMENT;
+    if (residual_stride < hidden) return MOE_ERR_INVALID_ARGUMENT;
+    if (hidden > kMaxHidden || num_tokens > MOE_BLOCK_NORM_MAX_TOKENS) return MOE_ERR_UNSUPPORTED;
+    if (num_tokens == 0) return MOE_OK;  // tensors without elements may be null
+    if ((normed != nullptr) != (pre_weight != nullptr)) return MOE_ERR_INVALID_ARGUMENT;
+    if (pre_rstd != nullptr && normed == nullptr) return MOE_ERR_INVALID_ARGUMENT;
+    const bool block = y != nullptr;
+    if (residual == nullptr || block != (res_out != nullptr)) return MOE_ERR_INVALID_ARGUMENT;
+    if (block) {
+        if (y_stride < hidden) return MOE_ERR_INVALID_ARGUMENT;
+    } else if (normed == nullptr || post_weight != nullptr || gate != nullptr || residual_scale != 1.0f) {
+        return MOE_ERR_INVALID_ARGUMENT;  // without a block only the norm before the next one is left
+    }
+    const int rb = dtype_bytes(residual_dtype), ab = dtype_bytes(act_dtype);
+    if (!aligned(residual, rb) || !aligned(res_out, rb) || !aligned(y, ab) || !aligned(normed, ab) ||
+        !aligned(post_weight, 4) || !aligned(gate, 4) || !aligned(pre_weight, 4) || !aligned(post_rstd, 4) ||
+        !aligned(pre_rstd, 4))
+        return MOE_ERR_INVALID_ARGUMENT;
+    const bool vec = hidden % 8 == 0 && vec_rows(residual, residual_stride, residual_dtype) &&
+                     vec_rows(y, y == nullptr ? 8 : y_stride, act_dtype) && aligned(res_out, 16) &&
+                     aligned(normed, 16) && aligned(post_weight, 16) && aligned(pre_weight, 16) &&
+                     (gate_mode != MOE_GATE_CHANNEL || aligned(gate, 16));
+    const NormArgs a{residual,  residual_stride, y,          y_stride, num_tokens, hidden, post_weight, gate,
+                     gate_mode, residual_scale,  pre_weight, eps,      res_out,    normed, post_rstd,   pre_rstd};
+    return hip_status(with_types(residual_dtype, act_dtype, [&](auto r, auto x) {
+        return launch_norm_types<decltype(r), decltype(x)>(a, vec, stream);
+    }));
+}
+
+size_t moe_block_norm_backward_workspace_bytes(int64_t num_tokens, int32_t hidden) {
+    if (num_tokens < 0 || num_tokens > MOE_BLOCK_NORM_MAX_TOKENS || hidden < 1 || hidden > moe::kMaxHidden) return 0;
+    const size_t n = static_cast<size_t>(moe::grad_blocks(num_tokens)) * 3 * static_cast<size_t>(hidden) * 4;
+    return (n + 255) / 256 * 256;
+}
+
+moe_status moe_block_norm_backward(const void* grad_res_out, const void* grad_normed, const void* res_out,
+                                   int64_t res_out_stride, int32_t residual_dtype, const void* y, int64_t y_stride,
+                                   int32_t act_dtype, int64_t num_tokens, int32_t hidden, const float* post_weight,
+                                   const float* gate, int32_t gate_mode, float residual_scale,
+                                   const float* pre_weight, const float* post_rstd, const float* pre_rstd,
+                                   void* grad_residual, void* grad_y, float* grad_post_weight, float* grad_gate,
+                                   float* grad_pre_weight, void* workspace, size_t workspace_bytes,
+                                   hipStream_t stream) {
+    using namespace moe;
+    if (num_tokens < 0 || hidden < 1 || !dtype_ok(residual_dtype) || !dtype_ok(act_dtype))
+        return MOE_ERR_INVALID_ARGUMENT;
+    if (gate_mode != MOE_GATE_NONE && gate_mode != MOE_GATE_CHANNEL && gate_mode != MOE_GATE_TOKEN)
+        return MOE_ERR_INVALID_ARGUMENT;
+    if (residual_scale != residual_scale) return MOE_ERR_INVALID_ARGUMENT;
+    if ((gate_mode != MOE_GATE_NONE) != (gate != nullptr) || (gate != nullptr) != (grad_gate != nullptr))
+        return MOE_ERR_INVALID_ARGUMENT;
+    if ((post_weight != nullptr) != (grad_post_weight != nullptr) ||
+        (pre_weight != nullptr) != (grad_pre_weight != nullptr))
+        return MOE_ERR_INVALID_ARGUMENT;
+    const bool pre = pre_weight != nullptr, block = y != nullptr;
+    if (pre && res_out_stride < hidden) return MOE_ERR_INVALID_ARGUMENT;
+    if (hidden > kMaxHidden || num_tokens > MOE_BLOCK_NORM_MAX_TOKENS) return MOE_ERR_UNSUPPORTED;
+    const int rb = dtype_bytes(residual_dtype), ab = dtype_bytes(act_dtype);
+    if (num_tokens > 0) {
+        if (grad_residual == nullptr || (grad_res_out == nullptr && !pre)) return MOE_ERR_INVALID_ARGUMENT;
+        if (block != (grad_y != nullptr)) return MOE_ERR_INVALID_ARGUMENT;
+        if (block) {
+            if (y_stride < hidden) return MOE_ERR_INVALID_ARGUMENT;
+        } else if (post_weight != nullptr || gate != nullptr || residual_scale != 1.0f) {
+            return MOE_ERR_INVALID_ARGUMENT;
+        }
+        if (pre ? (grad_normed == nullptr || res_out == nullptr || pre_rstd == nullptr) : grad_normed != nullptr)
+            return MOE_ERR_INVALID_ARGUMENT;
+        if (post_weight != nullptr && post_rstd == nullptr) return MOE_ERR_INVALID_ARGUMENT;
+        if (!aligned(grad_res_out, rb) || !aligned(res_out, rb) || !aligned(grad_residual, rb) ||
+            !aligned(grad_normed, ab) || !aligned(y, ab) || !aligned(grad_y, ab))
+            return MOE_ERR_INVALID_ARGUMENT;
+    }
+    for (const void* p : {static_cast<const void*>(post_weight), static_cast<const void*>(gate),
+                          static_cast<const void*>(pre_weight), static_cast<const void*>(post_rstd),
+                          static_cast<const void*>(pre_rstd), static_cast<const void*>(grad_post_weight),
+                          static_cast<const void*>(grad_gate), static_cast<const void*>(grad_pre_weight)})
+        if (!aligned(p, 4)) return MOE_ERR_INVALID_ARGUMENT;
+    const bool channel = gate_mode == MOE_GATE_CHANNEL;
+    const int params = (post_weight != nullptr) + channel + pre;
+    if (num_tokens > 0 && params > 0) {
+        if (workspace == nullptr || !aligned(workspace, 256)) return MOE_ERR_INVALID_ARGUMENT;
+        if (workspace_bytes < moe_block_norm_backward_workspace_bytes(num_tokens, hidden))
+            return MOE_ERR_WORKSPACE_TOO_SMALL;
+    }
+    const int64_t blocks = grad_blocks(num_tokens);
+    float* partials = static_cast<float*>(workspace);
+    if (num_tokens > 0) {
+        const bool vec = hidden % 8 == 0 && aligned(grad_res_out, 16) && aligned(grad_normed, 16) &&
+                         (!pre || vec_rows(res_out, res_out_stride, residual_dtype)) &&
+                         (!block || vec_rows(y, y_stride, act_dtype)) && aligned(grad_residual, 16) &&
+                         aligned(grad_y, 16) && aligned(post_weight, 16) && aligned(pre_weight, 16) &&
+                         (!channel || aligned(gate, 16));
+        const NormGradArgs a{grad_res_out,
+                             pre ? grad_normed : nullptr,
+                             res_out,
+                             res_out_stride,
+                             y,
+                             y_stride,
+                             num_tokens,
+                             hidden,
+                             post_weight,
+                             gate,
+                             gate_mode,
+                             residual_scale,
+                             pre_weight,
+                             post_rstd,
+                             pre_rstd,
+                             grad_residual,
+                             grad_y,
+                             gate_mode == MOE_GATE_TOKEN ? grad_gate : nullptr,
+                             partials,
+                             params};
+        const hipError_t err = with_types(residual_dtype, act_dtype, [&](auto r, auto x) {
+            return launch_grad_types<decltype(r), decltype(x)>(a, blocks, vec, stream);
+        });
+        if (err != hipSuccess) return hip_status(err);
+    }
+    if (params == 0) return MOE_OK;
+    // with no tokens the parameters' gradients are zero: the same sums over no workgroups
+    const int width = params * hidden;
+    hipLaunchKernelGGL(block_norm_param_kernel, dim3((width + kWave - 1) / kWave), dim3(kSumWaves * kWave), 0, stream,
+                       partials, blocks, width, hidden, grad_post_weight, channel ? grad_gate : nullptr,
+                       grad_pre_weight);
+    return hip_status(hipGetLastError());
+}
+
+}  // extern "C"
