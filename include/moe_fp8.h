@@ -524,7 +524,7 @@ moe_status moe_block_norm_backward(const void* grad_res_out, const void* grad_no
 
 #define MOE_SCORE_SOFTMAX 0 /* p = softmax(logits) */
 #define MOE_SCORE_SIGMOID 1 /* p = sigmoid(logits) / sum of the row's sigmoids */
-#define MOE_BALANCE_MAX_SEQS 65536
+#define MOE_BALANCE_MAX_SEQS 65535
 
 /* Bytes of device workspace moe_balance_loss needs (a multiple of 256).
  * Returns 0 for an invalid shape. */

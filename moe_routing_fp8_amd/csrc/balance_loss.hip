@@ -10,17 +10,24 @@
 //   g_s      = grad_loss[s] * E / (K n_s^2)
 // (the counts are whole numbers and carry no gradient).
 //
-// Forward, two launches.  The tokens are cut into chunks of consecutive
-// tokens, one workgroup each; a wave holds a token's whole row of logits in
-// registers and keeps its running sums of p there too.  A chunk may meet
+// Forward, two or three launches.  The tokens are cut into chunks of consecutive
+// tokens, one workgroup each; 16 lanes (64 above 256 experts) hold a token's
+// whole row of logits in registers and keep their running sums of p there
+// too.  A chunk may meet
 // several sequences: each (chunk, sequence) piece is summed over the
 // workgroup's waves in a fixed order and written to a slot of its own,
 // number chunk + sequence (along the pieces in token order either index
 // grows, so no two pieces share a slot, and a sequence's slots are
-// consecutive).  The second launch sums each sequence's slots in order.  No
-// floating atomics: the results do not depend on timing.
-// Backward, one launch: a wave per token reads the row again, with the
+// consecutive).  Then each sequence's slots are added in a fixed order: by one
+// workgroup per sequence in a second launch where it has few, else by
+// workgroups that take a few columns each, with the loss in a third launch.
+// No floating atomics: the results do not depend on timing.
+// Backward, one launch: the same lanes per token read the row again, with the
 // sequence's counts in registers.
+//
+// Sixteen lanes per row let the four row reductions of a wave run in the same
+// four DPP steps; with a row over all 64 lanes the reductions, six steps for
+// each row, took as many instructions as the exponentials.
 #include <hip/hip_runtime.h>
 
 #include "api_common.hpp"
@@ -30,17 +37,38 @@
 namespace moe {
 namespace {
 
-constexpr int kBalanceThreads = 256;
-constexpr int kBalanceWaves = kBalanceThreads / kWave;
-// Chunks of a large batch: two workgroups for each of the 256 compute units.
-constexpr int64_t kBalanceMaxChunks = 512;
-constexpr int64_t kBalanceMinChunkTokens = 8;
+constexpr int kMaxWaves = 16;
+constexpr int kNarrowExperts = 256;  // rows of up to this many experts lie over 16 lanes
+
+// How a row lies over the lanes: L lanes hold it, P values each; a wave has
+// 64 / L rows side by side.
+template <int L_, int P_>
+struct RowShape {
+    static constexpr int L = L_, P = P_;
+    static constexpr int kRows = kWave / L;
+};
+int rows_per_wave(int E) { return E > kNarrowExperts ? RowShape<64, 16>::kRows : RowShape<16, 16>::kRows; }
+
+// Chunks of a batch.  One sequence (or few): about one for each of the 256
+// compute units, since all their slots have to be added up for one result
+// (32768 tokens, 256 experts: sums and their reduction take 10.7 + 5.1 us in
+// 256 chunks, 15.3 + 6.4 us in 512).  Many sequences: smaller chunks, which
+// meet fewer of them one after another.
+constexpr int64_t kFewSeqsChunks = 256;
+constexpr int64_t kManySeqsChunks = 1024;
+constexpr int kManySeqs = 4;
+// Up to this many slots per sequence, on average, one workgroup adds all of a sequence's; above, its columns are
+// split over workgroups and the loss takes a launch of its own.
+constexpr int64_t kOneLevelSlots = 64;
+constexpr int kReduceCols = 16;  // columns of a workgroup of the split sum: 64-byte pieces of each slot
 
 struct BalancePlan {
-    int64_t chunk;       // tokens per workgroup
+    int waves;           // of a workgroup
+    int64_t chunk;       // tokens per workgroup: a multiple of waves * rows_per_wave
     int64_t num_chunks;
     int64_t num_slots;   // num_chunks + num_seqs
     size_t sums_bytes, counts_bytes, tokens_bytes;
+    size_t means_offset;  // a table [S, E] for calls that do not take prob_mean
     size_t workspace_bytes;
 };
 
@@ -48,14 +76,20 @@ size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 
 BalancePlan plan_balance(int64_t T, int E, int S) {
     BalancePlan p;
-    p.chunk = (T + kBalanceMaxChunks - 1) / kBalanceMaxChunks;
-    if (p.chunk < kBalanceMinChunkTokens) p.chunk = kBalanceMinChunkTokens;
+    const int64_t most = S >= kManySeqs ? kManySeqsChunks : kFewSeqsChunks;
+    const int64_t rows = rows_per_wave(E);
+    p.waves = 4;
+    while (p.waves < kMaxWaves && T > p.waves * rows * most) p.waves *= 2;
+    const int64_t step = p.waves * rows;
+    const int64_t steps = (T + step * most - 1) / (step * most);
+    p.chunk = step * (steps > 1 ? steps : 1);
     p.num_chunks = (T + p.chunk - 1) / p.chunk;
     p.num_slots = p.num_chunks + S;
     p.sums_bytes = round256(static_cast<size_t>(p.num_slots) * E * sizeof(float));
     p.counts_bytes = round256(static_cast<size_t>(p.num_slots) * E * sizeof(int32_t));
     p.tokens_bytes = round256(static_cast<size_t>(p.num_slots) * sizeof(int32_t));
-    p.workspace_bytes = p.sums_bytes + p.counts_bytes + p.tokens_bytes;
+    p.means_offset = p.sums_bytes + p.counts_bytes + p.tokens_bytes;
+    p.workspace_bytes = p.means_offset + round256(static_cast<size_t>(S) * E * sizeof(float));
     return p;
 }
 
@@ -76,117 +110,148 @@ struct Seqs {
     __device__ int find(int64_t t, int lane) const {
         if (offsets == nullptr) return 0;
         int n = 0;
-        for (int i = 1; i <= num_seqs; i += kWave) {
-            const bool before = i + lane <= num_seqs && edge(i + lane) <= t;
-            n += __builtin_popcountll(__ballot(before));
+        for (int i = 1 + lane; i - lane <= num_seqs; i += 4 * kWave) {
+            int32_t o[4];  // four loads in flight
+#pragma unroll
+            for (int k = 0; k < 4; ++k) o[k] = i + k * kWave <= num_seqs ? offsets[i + k * kWave] : INT32_MAX;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const bool before = i + k * kWave <= num_seqs && min(static_cast<int64_t>(o[k]), num_tokens) <= t;
+                n += __builtin_popcountll(__ballot(before));
+            }
         }
         return n;
     }
 };
 
-// A token's row over the wave: lane's experts are lane * P .. lane * P + P - 1
-// (VEC: E == 64 * P and aligned rows) or lane + 64 j.
-template <int P, bool VEC>
-__device__ __forceinline__ int expert_of(int lane, int j) { return VEC ? lane * P + j : lane + kWave * j; }
+// edge(i) for consecutive i, 64 of them held over the wave's lanes.
+struct EdgeWindow {
+    const Seqs& seqs;
+    int base;
+    int64_t held;  // of lane l: edge(base + l)
+    __device__ void load(int i, int lane) {
+        base = i;
+        held = seqs.edge(min(i + lane, seqs.num_seqs));
+    }
+    __device__ int64_t get(int i, int lane) {  // i uniform over the wave
+        if (i < base || i >= base + kWave) load(i, lane);
+        return __builtin_amdgcn_readlane(static_cast<int>(held), i - base);  // at most num_tokens < 2^31
+    }
+};
 
-template <typename TL, int P, bool VEC>
-__device__ __forceinline__ void load_row(const void* logits, int64_t at, int E, int lane, float (&z)[P]) {
-    if constexpr (VEC) {
-        TL::template load<P>(logits, at + lane * P, z);
-    } else {
+// The expert of lane l's j-th value: vectors of V in turn over the lanes.
+template <typename S, int V>
+__device__ __forceinline__ int expert_of(int l, int j) { return ((j / V) * S::L + l) * V + j % V; }
+
+// Lane l's values of a row of E (V > 1: E % V == 0 and aligned vectors); the padding gets `fill`.
+template <typename TL, typename S, int V>
+__device__ __forceinline__ void load_row(const void* p, int64_t at, int E, int l, float fill, float (&z)[S::P]) {
 #pragma unroll
-        for (int j = 0; j < P; ++j) {
-            const int e = lane + kWave * j;
-            float one[1] = {-INFINITY};
-            if (e < E) TL::template load<1>(logits, at + e, one);
-            z[j] = one[0];
-        }
+    for (int j = 0; j < S::P; j += V) {
+        const int e = expert_of<S, V>(l, j);
+        float v[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[i] = fill;
+        if (e < E) TL::template load<V>(p, at + e, v);
+#pragma unroll
+        for (int i = 0; i < V; ++i) z[j + i] = v[i];
+    }
+}
+template <typename TL, typename S, int V>
+__device__ __forceinline__ void store_row(void* p, int64_t at, int E, int l, const float (&d)[S::P]) {
+#pragma unroll
+    for (int j = 0; j < S::P; j += V) {
+        const int e = expert_of<S, V>(l, j);
+        float v[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[i] = d[j + i];
+        if (e < E) TL::template store<V>(p, at + e, v);
     }
 }
 
-// p of the row (0 at the padding, whose logit is -inf); comp[j] = 1 -
-// sigmoid(z[j]) with SIGMOID.  A row of nothing but -inf gives p = 0.
+// 1 / v for v in [1, 2]: the hardware's estimate and one Newton step (1 ulp).
+__device__ __forceinline__ float rcp_f32(float v) {
+    const float r = __builtin_amdgcn_rcpf(v);
+    return __builtin_fmaf(__builtin_fmaf(-v, r, 1.0f), r, r);
+}
+
+// The unnormalised scores w of a row (0 at the padding, whose logit is -inf)
+// and the factor that makes them p; comp = 1 - sigmoid(z) with SIGMOID.  A
+// row of nothing but -inf gives p = 0.
 //
 // sigmoid(z) = r or t r with t = exp(-|z|), r = 1 / (1 + t).  Where every
 // logit of a row is below -60 the sigmoids leave the range in which their
 // ratio keeps 24 bits, so they are taken relative to the largest logit m:
 // sigmoid(z) exp(-m) = exp(z - m) r.
-template <int P, bool SIGMOID>
-__device__ __forceinline__ void row_probs(const float (&z)[P], float (&p)[P], float (&comp)[P]) {
+template <typename S, bool SIGMOID>
+__device__ __forceinline__ float row_scores(const float (&z)[S::P], float (&w)[S::P], float (&comp)[S::P]) {
     float m = z[0];
 #pragma unroll
-    for (int j = 1; j < P; ++j) m = fmaxf(m, z[j]);
-    m = wave_max_f32(m);
+    for (int j = 1; j < S::P; ++j) m = fmaxf(m, z[j]);
+    m = group_max_f32<S::L>(m);
+    const bool nothing = m == -INFINITY;
+    if (nothing) m = 0.0f;
     float sum = 0.0f;
     if constexpr (SIGMOID) {
+        const bool low = m < -60.0f;
 #pragma unroll
-        for (int j = 0; j < P; ++j) {
+        for (int j = 0; j < S::P; ++j) {
             const float t = exp_nonpos(-fabsf(z[j]));
-            const float r = 1.0f / (1.0f + t);
-            p[j] = z[j] > 0.0f ? r : t * r;
+            const float r = rcp_f32(1.0f + t);
+            w[j] = z[j] > 0.0f ? r : t * r;
             comp[j] = z[j] > 0.0f ? t * r : r;
-            if (m < -60.0f) p[j] = exp_nonpos(z[j] - m) * r;
+            if (low) w[j] = exp_nonpos(z[j] - m) * r;
         }
     } else {
 #pragma unroll
-        for (int j = 0; j < P; ++j) p[j] = exp_nonpos(z[j] - m);
+        for (int j = 0; j < S::P; ++j) w[j] = exp_nonpos(z[j] - m);
     }
 #pragma unroll
-    for (int j = 0; j < P; ++j) sum += p[j];
-    sum = wave_sum_f32(sum);
-    const float inv = 1.0f / sum;
-#pragma unroll
-    for (int j = 0; j < P; ++j) p[j] = m == -INFINITY ? 0.0f : p[j] * inv;
+    for (int j = 0; j < S::P; ++j) sum += w[j];
+    sum = group_sum_f32<S::L>(sum);
+    return nothing ? 0.0f : 1.0f / sum;
 }
 
-template <typename TL, int P, bool VEC, bool SIGMOID>
-__global__ __launch_bounds__(kBalanceThreads) void balance_sums_kernel(
+template <typename TL, typename S, int V, bool SIGMOID>
+__global__ __launch_bounds__(kMaxWaves* kWave) void balance_sums_kernel(
     const void* __restrict__ logits, int64_t stride, int E, const int64_t* __restrict__ topk_idx, int K,
     const uint8_t* __restrict__ mask, Seqs seqs, int64_t chunk, float* __restrict__ sums,
     int32_t* __restrict__ counts, int32_t* __restrict__ tokens) {
-    extern __shared__ float lds[];  // kBalanceWaves x E sums, then E counts, then one token count
-    int32_t* hist = reinterpret_cast<int32_t*>(lds + kBalanceWaves * E);
+    constexpr int P = S::P;
+    extern __shared__ float lds[];  // waves x E sums, then E counts, then one token count
+    const int waves = blockDim.x / kWave;
+    int32_t* hist = reinterpret_cast<int32_t*>(lds + waves * E);
     int32_t* live = hist + E;
-    const int lane = threadIdx.x & (kWave - 1);
-    const int wave = threadIdx.x / kWave;
+    const int lane = threadIdx.x & (kWave - 1), l = lane % S::L, row = lane / S::L;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int64_t t0 = blockIdx.x * chunk;
     const int64_t t1 = min(t0 + chunk, seqs.num_tokens);
-    for (int e = threadIdx.x; e < E; e += kBalanceThreads) hist[e] = 0;
+    for (int e = threadIdx.x; e < E; e += blockDim.x) hist[e] = 0;
     if (threadIdx.x == 0) *live = 0;
-    __syncthreads();
-    for (int s = seqs.find(t0, lane); s < seqs.num_seqs; ++s) {
-        const int64_t begin = max(t0, seqs.edge(s)), end = min(t1, seqs.edge(s + 1));
-        if (begin >= t1) break;
-        if (begin >= end) continue;
-        float acc[P];
+
+    float acc[P];
 #pragma unroll
-        for (int j = 0; j < P; ++j) acc[j] = 0.0f;
-        int n = 0;
-        for (int64_t t = begin + wave; t < end; t += kBalanceWaves) {
-            if (mask != nullptr && mask[t] == 0) continue;
-            float z[P], p[P], comp[P];
-            load_row<TL, P, VEC>(logits, t * stride, E, lane, z);
-            if (lane < K) {
-                const int64_t id = topk_idx[t * K + lane];
-                if (id >= 0 && id < E) atomicAdd(&hist[id], 1);
-            }
-            row_probs<P, SIGMOID>(z, p, comp);
-#pragma unroll
-            for (int j = 0; j < P; ++j) acc[j] += p[j];
-            ++n;
-        }
+    for (int j = 0; j < P; ++j) acc[j] = 0.0f;
+    int n = 0;  // live tokens of the lane's row
+    int s = 0;
+    EdgeWindow edges{seqs, 0, 0};
+    // Writes sequence s's slot and starts afresh (every wave of the workgroup).
+    auto flush = [&]() {
 #pragma unroll
         for (int j = 0; j < P; ++j) {
-            const int e = expert_of<P, VEC>(lane, j);
-            if (e < E) lds[wave * E + e] = acc[j];
+            const int e = expert_of<S, V>(l, j);
+            if constexpr (S::L < kWave) acc[j] = join_rows(acc[j], [](float a, float b) { return a + b; });
+            if (row == 0 && e < E) lds[wave * E + e] = acc[j];
+            acc[j] = 0.0f;
         }
-        if (lane == 0) atomicAdd(live, n);
+        if (l == 0 && n != 0) atomicAdd(live, n);
+        n = 0;
         __syncthreads();
         const int64_t slot = blockIdx.x + static_cast<int64_t>(s);
-        for (int e = threadIdx.x; e < E; e += kBalanceThreads) {
+        for (int e = threadIdx.x; e < E; e += blockDim.x) {
             float v = 0.0f;
-#pragma unroll
-            for (int w = 0; w < kBalanceWaves; ++w) v += lds[w * E + e];
+#pragma unroll 4
+            for (int w = 0; w < waves; ++w) v += lds[w * E + e];
             sums[slot * E + e] = v;
             counts[slot * E + e] = hist[e];
             hist[e] = 0;
@@ -196,127 +261,285 @@ __global__ __launch_bounds__(kBalanceThreads) void balance_sums_kernel(
             *live = 0;
         }
         __syncthreads();
+    };
+
+    // A step's rows, masks and ids: none of them waits for the sequences, and
+    // the next step's are on their way while this one's are worked on.
+    float z[P];
+    int64_t id;  // of the lane's copy, l < K
+    bool on;
+    auto load_step = [&](int64_t t) {
+        const int64_t safe = min(t, t1 - 1);
+        load_row<TL, S, V>(logits, safe * stride, E, l, -INFINITY, z);
+        on = t < t1;
+        if (mask != nullptr) on = on && mask[safe] != 0;
+        id = -1;
+        if (l < K) id = topk_idx[safe * K + l];
+    };
+    const int64_t step = static_cast<int64_t>(waves) * S::kRows;
+    const int64_t ahead = wave * S::kRows + row;  // of the lane's token in a step
+    load_step(t0 + ahead);
+    s = seqs.find(t0, lane);
+    edges.load(s, lane);
+    __syncthreads();  // the counts are zero
+    for (int64_t g = t0; g < t1; g += step) {
+        const int64_t t = g + ahead;
+        float w[P], comp[P];
+        const float inv = row_scores<S, SIGMOID>(z, w, comp);
+        const int64_t now_id = id;
+        const bool now = on;
+        if (g + step < t1) load_step(t + step);
+        const int64_t gend = min(g + step, t1);
+        while (s < seqs.num_seqs) {
+            const int64_t begin = edges.get(s, lane), end = edges.get(s + 1, lane);
+            if (begin >= gend) break;
+            if (now && t >= begin && t < end) {
+                ++n;
+                if (now_id >= 0 && now_id < E) atomicAdd(&hist[now_id], 1);
+#pragma unroll
+                for (int j = 0; j < P; ++j) acc[j] = __builtin_fmaf(w[j], inv, acc[j]);
+            }
+            if (end > gend) break;  // the sequence goes on in the next step
+            if (max(begin, t0) < end) flush();
+            ++s;
+        }
     }
+    // the sequence that the chunk's end cuts
+    if (s < seqs.num_seqs && edges.get(s, lane) < t1 && edges.get(s + 1, lane) > t1) flush();
 }
 
-// One workgroup per sequence: its slots, in order.
-__global__ __launch_bounds__(kBalanceThreads) void balance_loss_kernel(
-    const float* __restrict__ sums, const int32_t* __restrict__ slot_counts,
-    const int32_t* __restrict__ slot_tokens, Seqs seqs, int64_t chunk, int E, int K, float* __restrict__ loss,
-    int32_t* __restrict__ counts, int32_t* __restrict__ seq_tokens, float* __restrict__ prob_mean) {
-    __shared__ float part[kBalanceWaves];
-    const int s = blockIdx.x;
+// The slots of sequence s: first .. last (first > last: none).
+__device__ __forceinline__ void seq_slots(const Seqs& seqs, int64_t chunk, int s, int64_t& first, int64_t& last) {
     const int64_t begin = seqs.edge(s), end = seqs.edge(s + 1);
-    int64_t first = 0, last = -1;  // slots
+    first = 0;
+    last = -1;
     if (begin < end) {
         first = begin / chunk + s;
         last = (end - 1) / chunk + s;
     }
+}
+
+// The lane's share of the live tokens of slots first .. last; wave_sum_i32 adds them.
+__device__ __forceinline__ int live_tokens(const int32_t* tokens, int64_t first, int64_t last, int lane) {
     int n = 0;
-    for (int64_t i = first; i <= last; ++i) n += slot_tokens[i];
-    const float many = n > 0 ? static_cast<float>(n) : 1.0f;
-    float dot = 0.0f;
-    for (int e = threadIdx.x; e < E; e += kBalanceThreads) {
-        float sum = 0.0f;
-        int c = 0;
-        for (int64_t i = first; i <= last; ++i) {
+    for (int64_t i = first + lane; i <= last; i += kWave) n += tokens[i];
+    return n;
+}
+
+// loss = E / (K n) * sum over e of count * mean, from the calling wave's lanes' parts of the sum.
+__device__ __forceinline__ float loss_value(float dot, int E, int K, float many) {
+    return dot * (static_cast<float>(E) / static_cast<float>(K)) / many;
+}
+
+// One workgroup per sequence: `cols` threads (a power of two >= E) for each
+// of blockDim / cols slots at a time; each thread's slots in order, then the
+// threads of a column in order, then the loss.
+__global__ __launch_bounds__(1024) void balance_loss_kernel(const float* __restrict__ sums,
+                                                             const int32_t* __restrict__ slot_counts,
+                                                             const int32_t* __restrict__ slot_tokens, Seqs seqs,
+                                                             int64_t chunk, int E, int K, int cols,
+                                                             float* __restrict__ loss, int32_t* __restrict__ counts,
+                                                             int32_t* __restrict__ seq_tokens,
+                                                             float* __restrict__ prob_mean) {
+    __shared__ float part[1024];
+    __shared__ int32_t part_count[1024];
+    __shared__ float part_dot[1024 / kWave];
+    const int s = blockIdx.x, lane = threadIdx.x & (kWave - 1);
+    const int e = threadIdx.x & (cols - 1), row = threadIdx.x / cols, rows = blockDim.x / cols;
+    int64_t first, last;
+    seq_slots(seqs, chunk, s, first, last);
+    int n = live_tokens(slot_tokens, first, last, lane);
+    float sum = 0.0f;
+    int c = 0;
+    if (e < E) {
+#pragma unroll 4
+        for (int64_t i = first + row; i <= last; i += rows) {
             sum += sums[i * E + e];
             c += slot_counts[i * E + e];
+        }
+    }
+    part[threadIdx.x] = sum;
+    part_count[threadIdx.x] = c;
+    n = wave_sum_i32(n);
+    const float many = n > 0 ? static_cast<float>(n) : 1.0f;
+    __syncthreads();
+    float dot = 0.0f;
+    if (row == 0 && e < E) {
+        for (int r = 1; r < rows; ++r) {
+            sum += part[r * cols + e];
+            c += part_count[r * cols + e];
         }
         const float mean = sum / many;
         counts[static_cast<int64_t>(s) * E + e] = c;
         if (prob_mean != nullptr) prob_mean[static_cast<int64_t>(s) * E + e] = mean;
-        dot += static_cast<float>(c) * mean;
+        dot = static_cast<float>(c) * mean;
     }
     dot = wave_sum_f32(dot);
-    if ((threadIdx.x & (kWave - 1)) == 0) part[threadIdx.x / kWave] = dot;
+    if (lane == 0) part_dot[threadIdx.x / kWave] = dot;
     __syncthreads();
     if (threadIdx.x == 0) {
-        float v = 0.0f;
-        for (int w = 0; w < kBalanceWaves; ++w) v += part[w];
-        loss[s] = v * (static_cast<float>(E) / static_cast<float>(K)) / many;
+        for (int w = 1; w < cols / kWave; ++w) dot += part_dot[w];
+        loss[s] = loss_value(dot, E, K, many);
         seq_tokens[s] = n;
     }
 }
 
-template <typename TL, int P, bool VEC, bool SIGMOID>
-__global__ __launch_bounds__(kBalanceThreads) void balance_grad_kernel(
-    const void* __restrict__ logits, int64_t stride, int E, int K, const uint8_t* __restrict__ mask, Seqs seqs,
-    int64_t chunk, const int32_t* __restrict__ counts, const int32_t* __restrict__ seq_tokens,
-    const float* __restrict__ grad_loss, void* __restrict__ grad) {
-    const int lane = threadIdx.x & (kWave - 1);
-    const int64_t first = (blockIdx.x * static_cast<int64_t>(kBalanceWaves) + threadIdx.x / kWave) * chunk;
-    const int64_t last = min(first + chunk, seqs.num_tokens);
-    if (first >= last) return;
-    int s = seqs.find(first, lane);
-    int held = -1;  // the sequence whose scaled counts are in a[]
-    float a[P];
-    for (int64_t t = first; t < last; ++t) {
-        while (s < seqs.num_seqs && seqs.edge(s + 1) <= t) ++s;
-        float d[P];
-        const bool live = s < seqs.num_seqs && seqs.edge(s) <= t && (mask == nullptr || mask[t] != 0);
-        if (live) {
-            if (held != s) {
-                held = s;
-                const float n = static_cast<float>(max(seq_tokens[s], 1));
-                const float g = grad_loss[s] * (static_cast<float>(E) / static_cast<float>(K)) / (n * n);
-#pragma unroll
-                for (int j = 0; j < P; ++j) {
-                    const int e = expert_of<P, VEC>(lane, j);
-                    a[j] = e < E ? g * static_cast<float>(counts[static_cast<int64_t>(s) * E + e]) : 0.0f;
-                }
-            }
-            float z[P], p[P], comp[P];
-            load_row<TL, P, VEC>(logits, t * stride, E, lane, z);
-            row_probs<P, SIGMOID>(z, p, comp);
-            float mean = 0.0f;
-#pragma unroll
-            for (int j = 0; j < P; ++j) mean += a[j] * p[j];
-            mean = wave_sum_f32(mean);
-#pragma unroll
-            for (int j = 0; j < P; ++j) {
-                d[j] = p[j] * (a[j] - mean);
-                if constexpr (SIGMOID) d[j] *= comp[j];
-            }
-        } else {
-#pragma unroll
-            for (int j = 0; j < P; ++j) d[j] = 0.0f;
+// A sequence of many chunks: a workgroup adds kReduceCols columns of one sequence's slots,
+// blockDim / kReduceCols of them at a time; each thread's slots in order, then
+// the threads of a column in order.  Leaves the means in `means` (prob_mean,
+// or a table of the workspace).
+__global__ __launch_bounds__(1024) void balance_reduce_kernel(const float* __restrict__ sums,
+                                                               const int32_t* __restrict__ slot_counts,
+                                                               const int32_t* __restrict__ slot_tokens, Seqs seqs,
+                                                               int64_t chunk, int E, int32_t* __restrict__ counts,
+                                                               int32_t* __restrict__ seq_tokens,
+                                                               float* __restrict__ means) {
+    __shared__ float part[1024];
+    __shared__ int32_t part_count[1024];
+    const int s = blockIdx.y;
+    const int col = threadIdx.x % kReduceCols, row = threadIdx.x / kReduceCols;
+    const int rows = blockDim.x / kReduceCols;
+    const int e = blockIdx.x * kReduceCols + col;
+    int64_t first, last;
+    seq_slots(seqs, chunk, s, first, last);
+    float sum = 0.0f;
+    int c = 0;
+    if (e < E) {
+#pragma unroll 4
+        for (int64_t i = first + row; i <= last; i += rows) {
+            sum += sums[i * E + e];
+            c += slot_counts[i * E + e];
         }
-        if constexpr (VEC) {
-            TL::template store<P>(grad, t * E + lane * P, d);
-        } else {
-#pragma unroll
-            for (int j = 0; j < P; ++j) {
-                const int e = lane + kWave * j;
-                const float one[1] = {d[j]};
-                if (e < E) TL::template store<1>(grad, t * E + e, one);
-            }
+    }
+    part[threadIdx.x] = sum;
+    part_count[threadIdx.x] = c;
+    __syncthreads();
+    if (threadIdx.x >= kWave) return;
+    const int n = wave_sum_i32(live_tokens(slot_tokens, first, last, threadIdx.x));
+    if (blockIdx.x == 0 && threadIdx.x == 0) seq_tokens[s] = n;
+    if (row == 0 && e < E) {
+        sum = 0.0f;
+        c = 0;
+        for (int r = 0; r < rows; ++r) {
+            sum += part[r * kReduceCols + col];
+            c += part_count[r * kReduceCols + col];
         }
+        counts[static_cast<int64_t>(s) * E + e] = c;
+        means[static_cast<int64_t>(s) * E + e] = sum / (n > 0 ? static_cast<float>(n) : 1.0f);
     }
 }
 
-// Calls f.template operator()<TL, P, VEC, SIGMOID>() for the row shape: P the
-// least power of two with 64 * P >= E, VEC where E == 64 * P and every
-// vector of P logits (and gradients) is aligned to min(16, its bytes).
-template <typename TL, int P, bool VEC, typename F>
-hipError_t with_score(int score, F&& f) {
-    return score == MOE_SCORE_SIGMOID ? f.template operator()<TL, P, VEC, true>()
-                                      : f.template operator()<TL, P, VEC, false>();
+// One wave per sequence: the loss from its counts and means.
+__global__ __launch_bounds__(256) void balance_dot_kernel(const int32_t* __restrict__ counts,
+                                                           const float* __restrict__ means,
+                                                           const int32_t* __restrict__ seq_tokens, int S, int E, int K,
+                                                           float* __restrict__ loss) {
+    const int lane = threadIdx.x & (kWave - 1);
+    const int s = blockIdx.x * (256 / kWave) + threadIdx.x / kWave;
+    if (s >= S) return;
+    const int64_t at = static_cast<int64_t>(s) * E;
+    float dot = 0.0f;
+    for (int e = lane; e < E; e += kWave) dot += static_cast<float>(counts[at + e]) * means[at + e];
+    dot = wave_sum_f32(dot);
+    const int n = seq_tokens[s];
+    if (lane == 0) loss[s] = loss_value(dot, E, K, n > 0 ? static_cast<float>(n) : 1.0f);
 }
-template <typename TL, int P, typename F>
-hipError_t with_vec(const void* logits, const void* grad, int64_t stride, int E, int score, F&& f) {
-    constexpr int bytes = P * TL::kBytes < 16 ? P * TL::kBytes : 16;
-    const bool vec = E == kWave * P && aligned(logits, bytes) && aligned(grad, bytes) &&
-                     stride * TL::kBytes % bytes == 0;
-    return vec ? with_score<TL, P, true>(score, f) : with_score<TL, P, false>(score, f);
+
+constexpr int kGradThreads = 256;
+// Waves of a large batch's gradient: 16 for each of the 256 compute units; a
+// wave then has the next set's loads in flight while it works on one.
+constexpr int64_t kGradWaves = 4096;
+
+// A wave takes `sets` sets of S::kRows consecutive tokens.
+template <typename TL, typename S, int V, bool SIGMOID>
+__global__ __launch_bounds__(kGradThreads) void balance_grad_kernel(
+    const void* __restrict__ logits, int64_t stride, int E, int K, const uint8_t* __restrict__ mask, Seqs seqs,
+    int64_t sets, const int32_t* __restrict__ counts, const int32_t* __restrict__ seq_tokens,
+    const float* __restrict__ grad_loss, void* __restrict__ grad) {
+    constexpr int P = S::P;
+    const int lane = threadIdx.x & (kWave - 1), l = lane % S::L, row = lane / S::L;
+    const int64_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const int64_t t0 = (blockIdx.x * static_cast<int64_t>(kGradThreads / kWave) + wave) * sets * S::kRows;
+    const int64_t t1 = min(t0 + sets * S::kRows, seqs.num_tokens);
+    if (t0 >= t1) return;
+    float z[P];
+    bool on;
+    auto load_set = [&](int64_t t) {
+        const int64_t safe = min(t, t1 - 1);
+        load_row<TL, S, V>(logits, safe * stride, E, l, -INFINITY, z);
+        on = t < t1;
+        if (mask != nullptr) on = on && mask[safe] != 0;
+    };
+    load_set(t0 + row);
+    int s = seqs.find(t0, lane);
+    EdgeWindow edges{seqs, 0, 0};
+    edges.load(s, lane);
+    int held = -1;  // the sequence whose scaled counts are in a[]
+    float a[P] = {};
+    for (int64_t g = t0; g < t1; g += S::kRows) {
+        float w[P], comp[P];
+        const float inv = row_scores<S, SIGMOID>(z, w, comp);
+        const bool now = on;
+        if (g + S::kRows < t1) load_set(g + S::kRows + row);
+        // each row's own sequence: step through the ends up to the set's last row
+        const int64_t t = g + row, last = min(g + S::kRows, t1) - 1;
+        while (s < seqs.num_seqs && edges.get(s + 1, lane) <= g) ++s;
+        int own = s;
+        int64_t begin = edges.get(s, lane);
+        for (int i = s; i < seqs.num_seqs; ++i) {
+            const int64_t end = edges.get(i + 1, lane);
+            if (end > last) break;
+            if (end <= t) {
+                own = i + 1;
+                begin = end;
+            }
+        }
+        const bool live = now && own < seqs.num_seqs && begin <= t;
+        if (__any(live && own != held)) {
+            held = min(own, seqs.num_seqs - 1);
+            const float n = static_cast<float>(max(seq_tokens[held], 1));
+            const float scale = grad_loss[held] * (static_cast<float>(E) / static_cast<float>(K)) / (n * n);
+            load_row<I32, S, V>(counts, static_cast<int64_t>(held) * E, E, l, 0.0f, a);
+#pragma unroll
+            for (int j = 0; j < P; ++j) a[j] *= scale;
+        }
+        float mean = 0.0f, d[P];
+#pragma unroll
+        for (int j = 0; j < P; ++j) mean = __builtin_fmaf(a[j], w[j], mean);
+        mean = group_sum_f32<S::L>(mean) * inv;
+#pragma unroll
+        for (int j = 0; j < P; ++j) {
+            d[j] = w[j] * inv * (a[j] - mean);
+            if constexpr (SIGMOID) d[j] *= comp[j];
+            d[j] = live ? d[j] : 0.0f;
+        }
+        if (t <= last) store_row<TL, S, V>(grad, t * E, E, l, d);
+    }
+}
+
+// Calls f.template operator()<TL, S, V, SIGMOID>() for the row shape.  V: 16
+// bytes of logits where every row starts on such a boundary (gradients and
+// counts as well) and E fills whole vectors, else single values.
+template <typename TL, typename S, typename F>
+hipError_t with_vec(bool vec, int score, F&& f) {
+    constexpr int V = S::P * TL::kBytes < 16 ? S::P : 16 / TL::kBytes;
+    if (vec)
+        return score == MOE_SCORE_SIGMOID ? f.template operator()<TL, S, V, true>()
+                                          : f.template operator()<TL, S, V, false>();
+    return score == MOE_SCORE_SIGMOID ? f.template operator()<TL, S, 1, true>()
+                                      : f.template operator()<TL, S, 1, false>();
 }
 template <typename TL, typename F>
-hipError_t with_row(const void* logits, const void* grad, int64_t stride, int E, int score, F&& f) {
-    if (E <= 64) return with_vec<TL, 1>(logits, grad, stride, E, score, f);
-    if (E <= 128) return with_vec<TL, 2>(logits, grad, stride, E, score, f);
-    if (E <= 256) return with_vec<TL, 4>(logits, grad, stride, E, score, f);
-    if (E <= 512) return with_vec<TL, 8>(logits, grad, stride, E, score, f);
-    return with_vec<TL, 16>(logits, grad, stride, E, score, f);
+hipError_t with_row(const void* logits, const void* grad, const void* counts, int64_t stride, int E, int score,
+                    F&& f) {
+    const bool vec = E >= 64 && E % (16 / TL::kBytes) == 0 && aligned(logits, 16) && aligned(grad, 16) &&
+                     aligned(counts, 16) && stride * TL::kBytes % 16 == 0;
+    if (E <= 16) return with_vec<TL, RowShape<16, 1>>(false, score, f);
+    if (E <= 64) return with_vec<TL, RowShape<16, 4>>(vec && TL::kBytes == 4, score, f);
+    if (E <= 128) return with_vec<TL, RowShape<16, 8>>(vec, score, f);
+    if (E <= kNarrowExperts) return with_vec<TL, RowShape<16, 16>>(vec, score, f);
+    if (E <= 512) return with_vec<TL, RowShape<64, 8>>(vec, score, f);
+    return with_vec<TL, RowShape<64, 16>>(vec, score, f);
 }
 
 struct SumsLauncher {
@@ -331,11 +554,11 @@ struct SumsLauncher {
     float* sums;
     int32_t *counts, *tokens;
     hipStream_t stream;
-    template <typename TL, int P, bool VEC, bool SIGMOID>
+    template <typename TL, typename S, int V, bool SIGMOID>
     hipError_t operator()() const {
-        const size_t lds = (static_cast<size_t>(kBalanceWaves + 1) * E + 1) * sizeof(float);
-        hipLaunchKernelGGL((balance_sums_kernel<TL, P, VEC, SIGMOID>), dim3(static_cast<unsigned>(plan.num_chunks)),
-                           dim3(kBalanceThreads), lds, stream, logits, stride, E, topk_idx, K, mask, seqs, plan.chunk,
+        const size_t lds = (static_cast<size_t>(plan.waves + 1) * E + 1) * sizeof(float);
+        hipLaunchKernelGGL((balance_sums_kernel<TL, S, V, SIGMOID>), dim3(static_cast<unsigned>(plan.num_chunks)),
+                           dim3(plan.waves * kWave), lds, stream, logits, stride, E, topk_idx, K, mask, seqs, plan.chunk,
                            sums, counts, tokens);
         return hipGetLastError();
     }
@@ -351,13 +574,14 @@ struct GradLauncher {
     const float* grad_loss;
     void* grad;
     hipStream_t stream;
-    template <typename TL, int P, bool VEC, bool SIGMOID>
+    template <typename TL, typename S, int V, bool SIGMOID>
     hipError_t operator()() const {
-        constexpr int64_t kChunk = 8;  // consecutive tokens of a wave
-        const int64_t per_block = kChunk * kBalanceWaves;
+        const int64_t all = (seqs.num_tokens + S::kRows - 1) / S::kRows;
+        const int64_t sets = (all + kGradWaves - 1) / kGradWaves;
+        const int64_t per_block = sets * S::kRows * (kGradThreads / kWave);
         const int64_t blocks = (seqs.num_tokens + per_block - 1) / per_block;
-        hipLaunchKernelGGL((balance_grad_kernel<TL, P, VEC, SIGMOID>), dim3(static_cast<unsigned>(blocks)),
-                           dim3(kBalanceThreads), 0, stream, logits, stride, E, K, mask, seqs, kChunk, counts,
+        hipLaunchKernelGGL((balance_grad_kernel<TL, S, V, SIGMOID>), dim3(static_cast<unsigned>(blocks)),
+                           dim3(kGradThreads), 0, stream, logits, stride, E, K, mask, seqs, sets, counts,
                            seq_tokens, grad_loss, grad);
         return hipGetLastError();
     }
@@ -413,12 +637,28 @@ moe_status moe_balance_loss(const void* logits, int32_t logits_dtype, int64_t ro
         const SumsLauncher go{logits, row_stride, num_experts, topk_idx, num_topk, token_mask, seqs,
                               plan,   sums,       slot_counts, slot_tokens, stream};
         const hipError_t err = logits_dtype == MOE_DTYPE_BF16
-                                   ? with_row<Bf16>(logits, nullptr, row_stride, num_experts, score, go)
-                                   : with_row<F32>(logits, nullptr, row_stride, num_experts, score, go);
+                                   ? with_row<Bf16>(logits, nullptr, nullptr, row_stride, num_experts, score, go)
+                                   : with_row<F32>(logits, nullptr, nullptr, row_stride, num_experts, score, go);
         if (err != hipSuccess) return hip_status(err);
     }
-    hipLaunchKernelGGL(balance_loss_kernel, dim3(num_seqs), dim3(kBalanceThreads), 0, stream, sums, slot_counts,
-                       slot_tokens, seqs, plan.chunk, num_experts, num_topk, loss, counts, seq_tokens, prob_mean);
+    const int64_t slots = plan.num_slots / num_seqs;  // of a sequence, on average
+    if (slots <= kOneLevelSlots) {
+        int cols = kWave, rows = 1;
+        while (cols < num_experts) cols *= 2;
+        while (rows < slots && cols * rows < 1024) rows *= 2;
+        hipLaunchKernelGGL(balance_loss_kernel, dim3(num_seqs), dim3(cols * rows), 0, stream, sums, slot_counts,
+                           slot_tokens, seqs, plan.chunk, num_experts, num_topk, cols, loss, counts, seq_tokens,
+                           prob_mean);
+        return hip_status(hipGetLastError());
+    }
+    float* means = prob_mean != nullptr ? prob_mean : reinterpret_cast<float*>(ws + plan.means_offset);
+    hipLaunchKernelGGL(balance_reduce_kernel, dim3((num_experts + kReduceCols - 1) / kReduceCols, num_seqs),
+                       dim3(1024), 0, stream, sums, slot_counts, slot_tokens, seqs, plan.chunk, num_experts, counts,
+                       seq_tokens, means);
+    const hipError_t err = hipGetLastError();
+    if (err != hipSuccess) return hip_status(err);
+    hipLaunchKernelGGL(balance_dot_kernel, dim3((num_seqs + 3) / 4), dim3(256), 0, stream, counts, means, seq_tokens,
+                       num_seqs, num_experts, num_topk, loss);
     return hip_status(hipGetLastError());
 }
 
@@ -441,8 +681,8 @@ moe_status moe_balance_loss_backward(const float* grad_loss, const void* logits,
     const GradLauncher go{logits, row_stride, num_experts, num_topk,    token_mask, seqs,
                           counts, seq_tokens, grad_loss,   grad_logits, stream};
     return hip_status(logits_dtype == MOE_DTYPE_BF16
-                          ? with_row<Bf16>(logits, grad_logits, row_stride, num_experts, score, go)
-                          : with_row<F32>(logits, grad_logits, row_stride, num_experts, score, go));
+                          ? with_row<Bf16>(logits, grad_logits, counts, row_stride, num_experts, score, go)
+                          : with_row<F32>(logits, grad_logits, counts, row_stride, num_experts, score, go));
 }
 
 }  // extern "C"

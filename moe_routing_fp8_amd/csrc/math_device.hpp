@@ -11,50 +11,62 @@ __device__ __forceinline__ float dpp_f32(float x) {
     return __uint_as_float(dpp_u32<CTRL>(__float_as_uint(x)));
 }
 
-// The value of the lane 16 places away in the other half of each 32-lane
-// half-wave (lane ^ 16), and of the lane in the other half-wave (lane ^ 32).
-__device__ __forceinline__ float lane_xor16(float x) {
-    return __int_as_float(__builtin_amdgcn_ds_swizzle(__float_as_int(x), 0x401F));
+// After the four steps within a 16-lane row, the rows meet through gfx950's
+// row and half-wave swaps: swapping a register with itself leaves, in the two
+// results, the two rows (halves) to be joined, in every lane.  VALU only; the
+// cross-lane moves through LDS (ds_swizzle, ds_bpermute) would add their
+// latency to each of the row reductions these kernels wait for.
+template <typename Op>
+__device__ __forceinline__ float join_rows(float x, Op op) {
+    const uint32_t b = __float_as_uint(x);
+    const auto rows = __builtin_amdgcn_permlane16_swap(b, b, false, false);
+    const uint32_t c = __float_as_uint(op(__uint_as_float(rows[0]), __uint_as_float(rows[1])));
+    const auto halves = __builtin_amdgcn_permlane32_swap(c, c, false, false);
+    return op(__uint_as_float(halves[0]), __uint_as_float(halves[1]));
 }
-__device__ __forceinline__ float lane_xor32(float x) { return __shfl_xor(x, 32, kWave); }
 
-// Sum over the wave in a fixed order; every lane receives it.
-__device__ __forceinline__ float wave_sum_f32(float x) {
+// Sum and maximum over each group of L lanes, 16 (a DPP row) or 64.
+template <int L>
+__device__ __forceinline__ float group_sum_f32(float x) {
+    static_assert(L == 16 || L == kWave, "a DPP row or a wave");
     x += dpp_f32<kDppQuadXor1>(x);
     x += dpp_f32<kDppQuadXor2>(x);
     x += dpp_f32<kDppRowHalfMirror>(x);
     x += dpp_f32<kDppRowMirror>(x);
-    x += lane_xor16(x);
-    x += lane_xor32(x);
+    if constexpr (L == kWave) x = join_rows(x, [](float a, float b) { return a + b; });
     return x;
 }
-
-// Maximum over the wave (a NaN loses to any number); every lane receives it.
-__device__ __forceinline__ float wave_max_f32(float x) {
+template <int L>
+__device__ __forceinline__ float group_max_f32(float x) {
+    static_assert(L == 16 || L == kWave, "a DPP row or a wave");
     x = fmaxf(x, dpp_f32<kDppQuadXor1>(x));
     x = fmaxf(x, dpp_f32<kDppQuadXor2>(x));
     x = fmaxf(x, dpp_f32<kDppRowHalfMirror>(x));
     x = fmaxf(x, dpp_f32<kDppRowMirror>(x));
-    x = fmaxf(x, lane_xor16(x));
-    x = fmaxf(x, lane_xor32(x));
+    if constexpr (L == kWave) x = join_rows(x, [](float a, float b) { return fmaxf(a, b); });
     return x;
 }
 
-// exp(x) for x <= 0 (and NaN): the hardware exp2 of the rounded product
-// x * log2(e), times a first-order correction by the product's rounding error
-// and the constant's low part.  Without it the error grows with |x| (the
-// argument of exp2 carries an error of |x| * 2^-25); with it the result is
-// within 2 ulp down to the smallest normal.  exp(-inf) = 0: the correction's
-// inf - inf is kept out by the select.
+// Sum over the wave in a fixed order; every lane receives it.
+__device__ __forceinline__ float wave_sum_f32(float x) { return group_sum_f32<kWave>(x); }
+
+__device__ __forceinline__ int wave_sum_i32(int x) {
+    uint32_t u = static_cast<uint32_t>(x);
+    u += dpp_u32<kDppQuadXor1>(u);
+    u += dpp_u32<kDppQuadXor2>(u);
+    u += dpp_u32<kDppRowHalfMirror>(u);
+    u += dpp_u32<kDppRowMirror>(u);
+    const auto rows = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+    u = rows[0] + rows[1];
+    const auto halves = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+    return static_cast<int>(halves[0] + halves[1]);
+}
+
+// exp(x) for x <= 0 (and NaN) by the hardware exp2: the rounded product x *
+// log2(e) costs a relative error of |x| * 2^-24 (about 1e-6 at x = -16, where
+// the value is 1e-7), which the scores' normalisation carries over unchanged.
 __device__ __forceinline__ float exp_nonpos(float x) {
-    constexpr float kLog2e = 1.44269504088896340736f;
-    constexpr float kLog2eLo = 1.9259629911266175e-8f;  // log2(e) - kLog2e
-    constexpr float kLn2 = 0.693147180559945309417f;
-    const float p = x * kLog2e;
-    float e = __builtin_fmaf(x, kLog2e, -p);
-    e = __builtin_fmaf(x, kLog2eLo, e);
-    const float r = __builtin_amdgcn_exp2f(p) * __builtin_fmaf(e, kLn2, 1.0f);
-    return x < -104.0f ? 0.0f : r;  // exp(-104) is below half the smallest denormal
+    return __builtin_amdgcn_exp2f(x * 1.44269504088896340736f);
 }
 
 // bf16 bit pattern (round to nearest even) of an fp32 value, and two packed.
@@ -141,6 +153,17 @@ struct F32 {
             static_assert(VEC == 1, "vector width");
             *q = f[0];
         }
+    }
+};
+
+// int32 values as fp32 (load only).
+struct I32 {
+    template <int VEC>
+    static __device__ __forceinline__ void load(const void* p, int64_t i, float (&f)[VEC]) {
+        float bits[VEC];
+        F32::load<VEC>(p, i, bits);
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) f[v] = static_cast<float>(__float_as_int(bits[v]));
     }
 };
 
