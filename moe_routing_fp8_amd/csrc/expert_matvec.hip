@@ -30,6 +30,8 @@
 // The workgroup's waves split k; their sums meet in LDS in a fixed order.
 #include <hip/hip_runtime.h>
 
+#include <type_traits>
+
 #include "api_common.hpp"
 #include "math_device.hpp"
 #include "moe_fp8.h"
@@ -42,6 +44,8 @@ typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
 typedef float f32x4_t __attribute__((ext_vector_type(4)));
 
 constexpr int kStep = 128;  // k per step of a wave
+constexpr int kMaxSplit = 8;  // waves that share a tile's k range
+constexpr int kMaxThreads = kMaxSplit * kWave;
 enum ScaleMode { kFolded = 0, kF32Group128 = 1, kF32Group32 = 2 };
 
 struct MatvecArgs {
@@ -61,7 +65,7 @@ struct MatvecArgs {
 union Frag {
     bf16x8_t v;
     bf16x2_t p[4];
-    uint4 u;
+    u32x4_t u;
 };
 
 // Eight e2m1 codes (low nibble first) times 2^(exponent of scale), as bf16.
@@ -127,167 +131,483 @@ __device__ __forceinline__ bool find_expert(const MatvecArgs& a, int index, int 
     return false;
 }
 
-template <bool E4M3, int MODE, int NT, int MT, int WAVES>
-__global__ __launch_bounds__(WAVES* kWave) void expert_matvec_kernel(MatvecArgs a) {
-    // the operand whose scale is per row of its own goes second: a lane's four
-    // sums then share that row
+__device__ __forceinline__ u32x4_t u32x4(uint32_t a, uint32_t b, uint32_t c, uint32_t d) { return u32x4_t{a, b, c, d}; }
+
+struct __attribute__((packed, aligned(4))) Words4 {  // four words, 4-byte aligned
+    uint32_t w[4];
+};
+struct __attribute__((packed, aligned(1))) Word {  // one word, any alignment
+    uint32_t w;
+};
+
+// One wave's share of a tile: NT * 16 weight rows from column n0 on, k steps
+// [first, last) of which [first, first + 4 * blocks) in blocks of four.
+struct Share {
+    int e, n0;
+    int64_t row0;  // of the expert's rows
+    int rows;
+    int first, blocks, last;
+};
+
+constexpr int kNT = 2;             // 16-column tiles of a wave
+constexpr int kCols = kNT * 16;
+constexpr int kBlock = 4;          // steps of a block: one 16-byte load of scales, and the depth of the loads in flight
+constexpr int kPair = 2;           // steps whose codes are loaded together: a row's 128 bytes, one cache line
+constexpr int kPitch = kCols + 1;  // floats of a row of sums in LDS
+constexpr int kSharedWaves = kBlock;  // waves of a workgroup that shares its x: one for each step of a block
+
+// LDS in 16-byte units.  Of each wave: codes of two steps, scales of a block
+// (kF32Group32: of a step), and its x of a step (private) or the workgroup's
+// x of a block (shared).  After the loop the sums of up to `rows` rows lie there.
+constexpr int kLdsCodes = kNT * kPair * kWave;
+constexpr int kLdsScales = kCols;
+constexpr int lds_x(bool shared, int rows) { return rows * 16 * (shared ? kBlock : 1); }
+constexpr int lds_wave(bool shared, int rows) { return kLdsCodes + kLdsScales + (shared ? 0 : lds_x(false, rows)); }
+constexpr size_t lds_bytes(bool shared, int rows, int waves) {
+    return sizeof(u32x4_t) * (static_cast<size_t>(waves) * lds_wave(shared, rows) + (shared ? lds_x(true, rows) : 0));
+}
+static_assert(32 * kPitch * 4 <= lds_wave(true, 32) * 16, "a wave's sums fit where its operands were");
+
+// Keeps the compiler from moving LDS accesses of one lane across those of
+// others that it has to stay behind; the hardware runs a wave's in order.
+__device__ __forceinline__ void wave_lds_order() {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+}
+
+// The sums of rows m0 .. m0 + ROWS - 1 of the expert over the wave's share of k.
+//
+// Eight neighbouring lanes load one row's 128 bytes of codes (16 neighbouring
+// lanes, or 8, a row's 256 or 128 bytes of x).  A load in the order of the
+// matrix fragments, whose neighbouring lanes lie in different rows, occupies
+// the address unit four times as long, and one that takes half a cache line
+// leaves the next step's to wait in the cache for the line on its way; either
+// bounded the kernel (as did one byte of scales per lane and step).  The wave's own corner of LDS then turns the data
+// into fragments: lane (lr, q) reads row lr.  The 16-byte chunks of a row are
+// stored at (chunk XOR row), which spreads the eight rows that one LDS clock
+// serves over all banks.
+//
+// SHARED: the workgroup's waves have tiles of their own and the same k, so
+// each loads the x of one step of a block for all of them; otherwise they
+// split k and each loads its own.
+template <bool E4M3, int MODE, int ROWS, bool SHARED>
+__device__ __forceinline__ void multiply_rows(const MatvecArgs& a, const Share& sh, int m0, int lane, int wave,
+                                              u32x4_t* lds, u32x4_t* x_lds, f32x4_t (&acc)[(ROWS + 15) / 16][kNT]) {
     constexpr bool kXFirst = MODE != kFolded;
-    __shared__ float red[WAVES > 1 ? WAVES : 1][MT * 16][NT * 16 + 1];
-    const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
+    constexpr int MT = (ROWS + 15) / 16;
+    constexpr int kChunks = E4M3 ? 8 : 16;             // 16-byte chunks of a row of x in a step
+    constexpr int kRowsPerLoad = kWave / kChunks;
+    constexpr int XI = (ROWS + kRowsPerLoad - 1) / kRowsPerLoad;
+    constexpr int kAhead = SHARED ? 1 : ROWS > 16 ? 2 : kBlock;  // steps of x in the wave's registers
+    constexpr int kStepX = ROWS * kChunks;             // LDS of a step's x
+    constexpr int XV = E4M3 ? 2 : 4;                   // 16-byte vectors of a lane's fragments of one step
     const int lr = lane & 15, q = lane >> 4;
-    int e, rows;
-    int64_t row0;
-    if (!find_expert(a, blockIdx.y, lane, e, row0, rows)) return;
-    const int n0 = blockIdx.x * (NT * 16);
     const int K = a.K;
-    const int steps = (K + kStep - 1) / kStep;
-    const int first = steps * wave / WAVES, last = steps * (wave + 1) / WAVES;
-    const int groups = K / a.group;
+    const bool bytes32 = MODE == kFolded && a.group == 32;
+    u32x4_t* lds_w = lds;
+    u32x4_t* lds_s = lds + kLdsCodes;
 
-    const uint8_t* wrow[NT];
-    int64_t srow[NT];  // first scale of the lane's weight row
+    // codes: load i's row 8 i + lane / 8 of tile nt, scales: row `lane` of the tile pair
+    const uint8_t* wp[kNT][kPair];
+    const int64_t row_e = static_cast<int64_t>(sh.e) * a.N;
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-        const int64_t n = static_cast<int64_t>(e) * a.N + min(n0 + nt * 16 + lr, a.N - 1);
-        wrow[nt] = a.codes + n * (K / 2) + q * 16;
-        srow[nt] = n * groups;
+    for (int nt = 0; nt < kNT; ++nt)
+#pragma unroll
+        for (int i = 0; i < kPair; ++i) {
+            const int64_t n = row_e + min(sh.n0 + nt * 16 + i * 8 + lane / 8, a.N - 1);
+            wp[nt][i] = a.codes + n * (K / 2) + ((lane & 7) ^ (lane >> 3)) * 16;
+        }
+    const uint8_t* sp = static_cast<const uint8_t*>(a.sf) + (row_e + min(sh.n0 + lane % kCols, a.N - 1)) *
+                                                               (K / a.group) * (MODE == kFolded ? 1 : 4);
+    // x: load i's row i * kRowsPerLoad + lane / kChunks
+    auto x_row = [&](int m) -> int64_t {
+        int64_t r = -1;
+        if (m0 + m < sh.rows && m < ROWS) r = a.row_token != nullptr ? a.row_token[sh.row0 + m0 + m] : sh.row0 + m0 + m;
+        return r < a.x_rows ? r : -1;
+    };
+    const uint8_t* xp[XI];
+#pragma unroll
+    for (int i = 0; i < XI; ++i) {
+        const int m = i * kRowsPerLoad + lane / kChunks;
+        const int64_t r = x_row(m);
+        xp[i] = r < 0 ? nullptr
+                      : static_cast<const uint8_t*>(a.x) + r * (E4M3 ? K : 2 * static_cast<int64_t>(K)) +
+                            ((lane ^ m) & (kChunks - 1)) * 16;
     }
-
-    for (int m0 = 0; m0 < rows; m0 += MT * 16) {
-        int64_t xrow[MT];  // x row of the lane's row of x, or -1
+    const float* xsp[MT];  // scales of e4m3 row lr of each fragment
+    if constexpr (E4M3)
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
-            const int m = m0 + mt * 16 + lr;
-            int64_t r = -1;
-            if (m < rows) r = a.row_token != nullptr ? a.row_token[row0 + m] : row0 + m;
-            xrow[mt] = r < a.x_rows ? r : -1;
+            const int64_t r = x_row(mt * 16 + lr);
+            xsp[mt] = r < 0 ? nullptr : a.x_sf + r * (K / 128);
         }
-        f32x4_t acc[MT][NT];
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) acc[mt][nt] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
 
-        for (int step = first; step < last; ++step) {
-            const int k0 = step * kStep;
-            const bool in = k0 + q * 32 < K;
-            uint32_t wd[NT][4];
-            float ws[NT][4];  // kFolded, kF32Group128: [0]
+    auto multiply = [&](const u32x4_t(&w)[kNT], const float(&ws)[kNT][4], const u32x4_t(&x)[MT][XV],
+                        const float(&xs_own)[MT]) __attribute__((always_inline)) {
+        bf16x8_t wf[kNT][4];
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                uint4 w = make_uint4(0, 0, 0, 0);
-                if (in) w = *reinterpret_cast<const uint4*>(wrow[nt] + k0 / 2);
-                wd[nt][0] = w.x; wd[nt][1] = w.y; wd[nt][2] = w.z; wd[nt][3] = w.w;
-                ws[nt][0] = 1.0f;
-                if constexpr (MODE == kFolded) {
-                    if (in) {
-                        const uint32_t b = static_cast<const uint8_t*>(a.sf)[srow[nt] + (k0 + q * 32) / a.group];
-                        ws[nt][0] = __uint_as_float(b << 23);
-                    }
-                } else if constexpr (MODE == kF32Group128) {
-                    ws[nt][0] = static_cast<const float*>(a.sf)[srow[nt] + k0 / 128];
-                } else {
+        for (int nt = 0; nt < kNT; ++nt) {
+            uint32_t d[4] = {w[nt].x, w[nt].y, w[nt].z, w[nt].w};
+            if constexpr (MODE == kF32Group32) transpose_quarters(d);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        ws[nt][i] = k0 + i * 32 < K ? static_cast<const float*>(a.sf)[srow[nt] + k0 / 32 + i] : 0.0f;
-                    transpose_quarters(wd[nt]);
-                }
-            }
+            for (int i = 0; i < 4; ++i) wf[nt][i] = e2m1_to_bf16(d[i], MODE == kFolded ? ws[nt][0] : 1.0f);
+        }
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
-                // the lane's k of instruction i start at ks + i * ki
-                const int ks = MODE == kF32Group32 ? k0 + q * 8 : k0 + q * 32;
-                constexpr int ki = MODE == kF32Group32 ? 32 : 8;
-                bf16x8_t xf[4];
-                float xs[4] = {1.0f, 1.0f, 1.0f, 1.0f};  // kXFirst: of the lane's four sums' rows; else [0]
+        for (int mt = 0; mt < MT; ++mt) {
+            bf16x8_t xf[4];
+            if constexpr (E4M3) {
+                xf[0] = e4m3_to_bf16(x[mt][0].x, x[mt][0].y);
+                xf[1] = e4m3_to_bf16(x[mt][0].z, x[mt][0].w);
+                xf[2] = e4m3_to_bf16(x[mt][1].x, x[mt][1].y);
+                xf[3] = e4m3_to_bf16(x[mt][1].z, x[mt][1].w);
+            } else {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     Frag f;
-                    f.u = make_uint4(0, 0, 0, 0);
-                    if (xrow[mt] >= 0 && ks + i * ki < K) {
-                        if constexpr (E4M3) {
-                            const uint2 c = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(a.x) +
-                                                                            xrow[mt] * K + ks + i * ki);
-                            f.v = e4m3_to_bf16(c.x, c.y);
-                        } else {
-                            f.u = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.x) + xrow[mt] * K +
-                                                                  ks + i * ki);
-                        }
-                    }
+                    f.u = x[mt][i];
                     xf[i] = f.v;
                 }
-                if constexpr (E4M3) {
-                    float own = 0.0f;
-                    if (xrow[mt] >= 0) own = a.x_sf[xrow[mt] * (K / 128) + step];
-                    xs[0] = own;
-                    if constexpr (kXFirst) {
+            }
+            float xs[4] = {1.0f, 1.0f, 1.0f, 1.0f};  // kXFirst: of the lane's four sums' rows; else [0]
+            if constexpr (E4M3) {
+                xs[0] = xs_own[mt];
+                if constexpr (kXFirst) {
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) xs[j] = __shfl(own, q * 4 + j, kWave);
-                    }
+                    for (int j = 0; j < 4; ++j) xs[j] = __shfl(xs_own[mt], q * 4 + j, kWave);
                 }
+            }
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    if constexpr (MODE == kFolded) {
-                        f32x4_t d = E4M3 ? f32x4_t{0.0f, 0.0f, 0.0f, 0.0f} : acc[mt][nt];
+            for (int nt = 0; nt < kNT; ++nt) {
+                if constexpr (MODE == kFolded) {
+                    f32x4_t d = E4M3 ? f32x4_t{0.0f, 0.0f, 0.0f, 0.0f} : acc[mt][nt];
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(e2m1_to_bf16(wd[nt][i], ws[nt][0]), xf[i], d,
-                                                                        0, 0, 0);
+                    for (int i = 0; i < 4; ++i)
+                        d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wf[nt][i], xf[i], d, 0, 0, 0);
 #pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            acc[mt][nt][j] = E4M3 ? __builtin_fmaf(xs[0], d[j], acc[mt][nt][j]) : d[j];
-                    } else if constexpr (MODE == kF32Group128) {
+                    for (int j = 0; j < 4; ++j)
+                        acc[mt][nt][j] = E4M3 ? __builtin_fmaf(xs[0], d[j], acc[mt][nt][j]) : d[j];
+                } else if constexpr (MODE == kF32Group128) {
+                    f32x4_t d = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf[i], wf[nt][i], d, 0, 0, 0);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        acc[mt][nt][j] = __builtin_fmaf(ws[nt][0] * xs[j], d[j], acc[mt][nt][j]);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
                         f32x4_t d = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf[i], e2m1_to_bf16(wd[nt][i], 1.0f), d, 0, 0,
-                                                                        0);
+                        d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf[i], wf[nt][i], d, 0, 0, 0);
 #pragma unroll
                         for (int j = 0; j < 4; ++j)
-                            acc[mt][nt][j] = __builtin_fmaf(ws[nt][0] * xs[j], d[j], acc[mt][nt][j]);
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            f32x4_t d = {0.0f, 0.0f, 0.0f, 0.0f};
-                            d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf[i], e2m1_to_bf16(wd[nt][i], 1.0f), d, 0, 0,
-                                                                        0);
-#pragma unroll
-                            for (int j = 0; j < 4; ++j)
-                                acc[mt][nt][j] = __builtin_fmaf(ws[nt][i] * xs[j], d[j], acc[mt][nt][j]);
-                        }
+                            acc[mt][nt][j] = __builtin_fmaf(ws[nt][i] * xs[j], d[j], acc[mt][nt][j]);
                     }
                 }
             }
         }
+    };
+
+    // Loads complete in order, so a step's x goes out before its codes.  Lanes without a row of x load nothing:
+    // their fragment rows hold anything, and only give sums that are not kept.
+    auto load_x = [&](u32x4_t(&x)[XI], int step) __attribute__((always_inline)) {
+#pragma unroll
+        for (int i = 0; i < XI; ++i)
+            if (xp[i] != nullptr)
+                x[i] = *reinterpret_cast<const u32x4_t*>(xp[i] + static_cast<int64_t>(step) * (kChunks * 16));
+    };
+    auto load_codes = [&](u32x4_t(&w)[kNT][kPair], int step) __attribute__((always_inline)) {
+#pragma unroll
+        for (int nt = 0; nt < kNT; ++nt)
+#pragma unroll
+            for (int i = 0; i < kPair; ++i)
+                w[nt][i] = __builtin_nontemporal_load(
+                    reinterpret_cast<const u32x4_t*>(wp[nt][i] + step * (kStep / 2)));
+    };
+    auto load_step_scales = [&](u32x4_t& s, int step) __attribute__((always_inline)) {
+        if (MODE == kF32Group32 && lane < kCols) {
+            const Words4 v = *reinterpret_cast<const Words4*>(sp + 16 * step);
+            s = u32x4(v.w[0], v.w[1], v.w[2], v.w[3]);
+        }
+    };
+    // a block's scales of a weight row: 16 bytes, or one word of four steps' bytes
+    auto load_scales = [&](u32x4_t& s, float4(&xs)[MT], int step) __attribute__((always_inline)) {
+        if (MODE != kF32Group32 && lane < kCols) {
+            if (MODE == kFolded && !bytes32) {
+                s.x = reinterpret_cast<const Word*>(sp + step)->w;
+            } else {
+                const Words4 v = *reinterpret_cast<const Words4*>(sp + 4 * step);
+                s = u32x4(v.w[0], v.w[1], v.w[2], v.w[3]);
+            }
+        }
+        if constexpr (E4M3)
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+                if (xsp[mt] != nullptr) {
+                    const Words4 v = *reinterpret_cast<const Words4*>(xsp[mt] + step);
+                    xs[mt] = make_float4(__uint_as_float(v.w[0]), __uint_as_float(v.w[1]), __uint_as_float(v.w[2]),
+                                         __uint_as_float(v.w[3]));
+                }
+    };
+    if (sh.blocks > 0) {
+        u32x4_t w[kBlock / kPair][kNT][kPair], x[kAhead][XI], s[kBlock];  // s: kF32Group32 of each step
+        float4 xs[MT] = {}, xs_next[MT] = {};
+        u32x4_t s_next;
+        const int end = sh.first + kBlock * sh.blocks;
+        load_scales(s_next, xs_next, sh.first);
+#pragma unroll
+        for (int j = 0; j < kBlock; ++j) {
+            if (j < kAhead) load_x(x[j], sh.first + (SHARED ? wave : j));
+            load_step_scales(s[j], sh.first + j);
+            if (j % kPair == 0) load_codes(w[j / kPair], sh.first + j);
+        }
+        for (int step = sh.first; step < end; step += kBlock) {
+            const bool more = step + kBlock < end;
+            if (MODE != kF32Group32 && lane < kCols) lds_s[lane] = s_next;
+            if constexpr (E4M3)
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt) xs[mt] = xs_next[mt];
+            if (more) load_scales(s_next, xs_next, step + kBlock);
+            if constexpr (SHARED) {
+                if (step > sh.first) __syncthreads();  // the block before has been read
+#pragma unroll
+                for (int i = 0; i < XI; ++i) x_lds[wave * kStepX + i * kWave + lane] = x[0][i];
+                if (more) load_x(x[0], step + kBlock + wave);
+                __syncthreads();
+            }
+#pragma unroll
+            for (int j = 0; j < kBlock; ++j) {
+                if (j % kPair == 0)
+#pragma unroll
+                    for (int nt = 0; nt < kNT; ++nt)
+#pragma unroll
+                        for (int i = 0; i < kPair; ++i)
+                            lds_w[(nt * kPair + i) * kWave + lane] = w[j / kPair][nt][i];
+                if constexpr (!SHARED)
+#pragma unroll
+                    for (int i = 0; i < XI; ++i) x_lds[i * kWave + lane] = x[j % kAhead][i];
+                if (MODE == kF32Group32 && lane < kCols) lds_s[lane] = s[j];
+                if constexpr (!SHARED)
+                    if (j + kAhead < kBlock || more) load_x(x[j % kAhead], step + j + kAhead);
+                if (more) {
+                    load_step_scales(s[j], step + kBlock + j);
+                    if (j % kPair == 0) load_codes(w[j / kPair], step + kBlock + j);
+                }
+                wave_lds_order();
+                u32x4_t wl[kNT], xl[MT][XV];
+                float ws[kNT][4], xs_step[MT];
+#pragma unroll
+                for (int nt = 0; nt < kNT; ++nt) {
+                    wl[nt] = lds_w[nt * (kPair * kWave) + lr * 8 + ((j % kPair * 4 + q) ^ (lr & 7))];
+                    const uint32_t* sw = reinterpret_cast<const uint32_t*>(lds_s + nt * 16 + lr);
+                    if constexpr (MODE == kFolded) {
+                        const uint32_t v = bytes32 ? sw[j] >> (8 * q) : sw[0] >> (8 * j);
+                        ws[nt][0] = __uint_as_float((v & 0xFFu) << 23);
+                    } else if constexpr (MODE == kF32Group128) {
+                        ws[nt][0] = __uint_as_float(sw[j]);
+                    } else {
+                        const u32x4_t v = lds_s[nt * 16 + lr];
+                        ws[nt][0] = __uint_as_float(v.x);
+                        ws[nt][1] = __uint_as_float(v.y);
+                        ws[nt][2] = __uint_as_float(v.z);
+                        ws[nt][3] = __uint_as_float(v.w);
+                    }
+                }
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt) {
+                    const int m = mt * 16 + lr;
+                    const u32x4_t* row = x_lds + (SHARED ? j * kStepX : 0) + m * kChunks;
+                    if constexpr (MODE == kF32Group32 && E4M3) {  // k = 32 i + 8 q of instruction i: half a chunk
+                        u32x2_t c[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            c[i] = reinterpret_cast<const u32x2_t*>(row + ((2 * i + (q >> 1)) ^ (m & 7)))[q & 1];
+                        xl[mt][0] = u32x4(c[0].x, c[0].y, c[1].x, c[1].y);
+                        xl[mt][1] = u32x4(c[2].x, c[2].y, c[3].x, c[3].y);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < XV; ++i)
+                            xl[mt][i] = row[(MODE == kF32Group32 ? 4 * i + q : XV * q + i) ^ (m & (kChunks - 1))];
+                    }
+                    xs_step[mt] = j == 0 ? xs[mt].x : j == 1 ? xs[mt].y : j == 2 ? xs[mt].z : xs[mt].w;
+                }
+                wave_lds_order();
+                multiply(wl, ws, xl, xs_step);
+                __builtin_amdgcn_sched_barrier(0);  // the next step's fragments would not fit the registers as well
+            }
+        }
+    }
+    // What is left, one step at a time and straight into fragments; the last may end inside (K % 128 != 0).
+    if (sh.first + kBlock * sh.blocks >= sh.last) return;
+    int64_t frag_row[MT];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) frag_row[mt] = x_row(mt * 16 + lr);
+    for (int step = sh.first + kBlock * sh.blocks; step < sh.last; ++step) {
+        const int k0 = step * kStep;
+        u32x4_t w[kNT], x[MT][XV] = {};
+        float ws[kNT][4], xs[MT] = {};
+        const bool in = k0 + q * 32 < K;
+#pragma unroll
+        for (int nt = 0; nt < kNT; ++nt) {
+            const int64_t n = row_e + min(sh.n0 + nt * 16 + lr, a.N - 1);
+            w[nt] = u32x4(0, 0, 0, 0);
+            if (in) w[nt] = *reinterpret_cast<const u32x4_t*>(a.codes + n * (K / 2) + k0 / 2 + q * 16);
+            if constexpr (MODE == kFolded) {
+                ws[nt][0] = 1.0f;
+                if (in)
+                    ws[nt][0] = __uint_as_float(
+                        static_cast<uint32_t>(
+                            static_cast<const uint8_t*>(a.sf)[n * (K / a.group) + (k0 + q * 32) / a.group])
+                        << 23);
+            } else if constexpr (MODE == kF32Group128) {
+                ws[nt][0] = static_cast<const float*>(a.sf)[n * (K / 128) + step];
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    ws[nt][i] = k0 + i * 32 < K ? static_cast<const float*>(a.sf)[n * (K / 32) + 4 * step + i] : 0.0f;
+            }
+        }
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+            if (frag_row[mt] < 0) continue;
+            if constexpr (E4M3) {
+                xs[mt] = a.x_sf[frag_row[mt] * (K / 128) + step];
+                const uint8_t* p = static_cast<const uint8_t*>(a.x) + frag_row[mt] * K + k0;
+                if constexpr (MODE == kF32Group32) {
+                    u32x2_t c[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) c[i] = *reinterpret_cast<const u32x2_t*>(p + 32 * i + 8 * q);
+                    x[mt][0] = u32x4(c[0].x, c[0].y, c[1].x, c[1].y);
+                    x[mt][1] = u32x4(c[2].x, c[2].y, c[3].x, c[3].y);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) x[mt][i] = *reinterpret_cast<const u32x4_t*>(p + 32 * q + 16 * i);
+                }
+            } else {
+                const uint16_t* p = static_cast<const uint16_t*>(a.x) + frag_row[mt] * K + k0;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int k = MODE == kF32Group32 ? 32 * i + 8 * q : 32 * q + 8 * i;
+                    if (k0 + k < K) x[mt][i] = *reinterpret_cast<const u32x4_t*>(p + k);
+                }
+            }
+        }
+        multiply(w, ws, x, xs);
+    }
+}
+
+// A workgroup is blockDim / 64 waves.  SHARED: each has a tile of kCols output
+// columns of its own; otherwise they split the k range of one tile.  MAXROWS:
+// rows that one pass over the weights serves; an expert with more takes
+// several.
+template <bool E4M3, int MODE, int MAXROWS, bool SHARED>
+__global__ __launch_bounds__(kMaxThreads) void expert_matvec_kernel(MatvecArgs a) {
+    // the operand whose scale is per row of its own goes second: a lane's four
+    // sums then share that row
+    constexpr bool kXFirst = MODE != kFolded;
+    constexpr int kLdsWave = lds_wave(SHARED, MAXROWS);
+    extern __shared__ u32x4_t lds[];
+    const int lane = threadIdx.x & (kWave - 1);
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const int waves = blockDim.x / kWave;
+    const int lr = lane & 15, q = lane >> 4;
+    Share sh;
+    if (!find_expert(a, blockIdx.y, lane, sh.e, sh.row0, sh.rows)) return;
+    const int split = SHARED ? 1 : waves, part = SHARED ? 0 : wave;
+    sh.n0 = (SHARED ? blockIdx.x * waves + wave : blockIdx.x) * kCols;  // may be past N: then nothing is written
+    const int steps = (a.K + kStep - 1) / kStep;
+    // blocks need whole steps and, for the scales' words, rows of whole words
+    const int blocks = a.K % kStep == 0 ? steps / kBlock : 0;
+    if (a.x_rows == 0) {
+        sh.first = sh.blocks = sh.last = 0;
+    } else if (blocks > 0) {
+        sh.first = blocks * part / split * kBlock;
+        sh.blocks = blocks * (part + 1) / split - blocks * part / split;
+        sh.last = part == split - 1 ? steps : sh.first + kBlock * sh.blocks;
+    } else {
+        sh.first = steps * part / split;
+        sh.last = steps * (part + 1) / split;
+        sh.blocks = 0;
+    }
+
+    // Leaves the wave's sums in LDS, adds the shares of the tile's waves in order and writes the rows.
+    u32x4_t* mine = lds + wave * kLdsWave;
+    u32x4_t* x_lds = SHARED ? lds + waves * kLdsWave : mine + kLdsCodes + kLdsScales;
+    const float* tile = reinterpret_cast<const float*>(lds + (wave - part) * kLdsWave);
+    auto run = [&](auto rows_const, int m0) __attribute__((always_inline)) {
+        constexpr int ROWS = decltype(rows_const)::value;
+        constexpr int MT = (ROWS + 15) / 16;
+        f32x4_t acc[MT][kNT] = {};
+        multiply_rows<E4M3, MODE, ROWS, SHARED>(a, sh, m0, lane, wave, mine, x_lds, acc);
+        wave_lds_order();
+        float* sums = reinterpret_cast<float*>(mine);
         // the first operand's rows run along a lane's sums, the second's along the lanes
-        if (m0 > 0) __syncthreads();
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+            for (int nt = 0; nt < kNT; ++nt)
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    red[wave][mt * 16 + (kXFirst ? q * 4 + j : lr)][nt * 16 + (kXFirst ? lr : q * 4 + j)] =
-                        acc[mt][nt][j];
-        __syncthreads();
-        for (int i = threadIdx.x; i < MT * 16 * NT * 16; i += WAVES * kWave) {
-            const int m = i / (NT * 16), n = i % (NT * 16);
-            if (m0 + m >= rows || n0 + n >= a.N) continue;
+                for (int i = 0; i < 4; ++i)
+                    sums[(mt * 16 + (kXFirst ? q * 4 + i : lr)) * kPitch + nt * 16 + (kXFirst ? lr : q * 4 + i)] =
+                        acc[mt][nt][i];
+        if constexpr (SHARED)
+            wave_lds_order();
+        else
+            __syncthreads();
+        for (int i = part * kWave + lane; i < ROWS * kCols; i += split * kWave) {
+            const int m = i / kCols, n = i % kCols;
+            if (m0 + m >= sh.rows || sh.n0 + n >= a.N) continue;
             float v = 0.0f;
-#pragma unroll
-            for (int w = 0; w < WAVES; ++w) v += red[w][m][n];
-            a.out[(row0 + m0 + m) * a.N + n0 + n] = bf16_bits(v);
+            for (int w = 0; w < split; ++w) v += tile[w * (kLdsWave * 4) + m * kPitch + n];
+            const int64_t r = sh.row0 + m0 + m;
+            if (a.row_token != nullptr) {
+                const int t = a.row_token[r];
+                if (t < 0 || t >= a.x_rows) v = 0.0f;
+            }
+            a.out[r * a.N + sh.n0 + n] = bf16_bits(v);
         }
+    };
+    for (int m0 = 0; m0 < sh.rows; m0 += MAXROWS) {
+        if (m0 > 0) __syncthreads();  // the sums and operands in LDS have been read
+        const int rows = sh.rows - m0;
+        if (!E4M3 && MAXROWS <= 8 && rows <= 4)
+            run(std::integral_constant<int, 4>{}, m0);
+        else if (MAXROWS <= 8 || rows <= 8)
+            run(std::integral_constant<int, 8>{}, m0);
+        else if (rows <= 16)
+            run(std::integral_constant<int, MAXROWS < 16 ? MAXROWS : 16>{}, m0);
+        else
+            run(std::integral_constant<int, MAXROWS>{}, m0);
     }
+}
+
+template <bool E4M3, int MODE, int MAXROWS>
+hipError_t launch_rows(const MatvecArgs& a, int64_t experts, hipStream_t stream) {
+    const int64_t tiles = (a.N + kCols - 1) / kCols;
+    const int blocks = a.K / (kStep * kBlock);
+    // A wave for each tile where that gives every compute unit eight waves and more; else the waves of a workgroup
+    // split k, as far as there is a block of steps for each.
+    if (tiles * experts >= 2048 || blocks < 2) {
+        const dim3 grid(static_cast<unsigned>((tiles + kSharedWaves - 1) / kSharedWaves),
+                        static_cast<unsigned>(experts));
+        hipLaunchKernelGGL((expert_matvec_kernel<E4M3, MODE, MAXROWS, true>), grid, dim3(kSharedWaves * kWave),
+                           lds_bytes(true, MAXROWS, kSharedWaves), stream, a);
+    } else {
+        int split = 2;
+        while (split < kMaxSplit && tiles * experts * split < 4096 && blocks >= 2 * split) split *= 2;
+        hipLaunchKernelGGL((expert_matvec_kernel<E4M3, MODE, MAXROWS, false>),
+                           dim3(static_cast<unsigned>(tiles), static_cast<unsigned>(experts)), dim3(split * kWave),
+                           lds_bytes(false, MAXROWS, split), stream, a);
+    }
+    return hipGetLastError();
 }
 
 template <bool E4M3, int MODE>
 hipError_t launch_matvec(const MatvecArgs& a, hipStream_t stream) {
-    constexpr int NT = 2, MT = 1, WAVES = 4;
-    const unsigned experts = static_cast<unsigned>(a.E < a.num_rows ? a.E : a.num_rows);
-    const dim3 grid(static_cast<unsigned>((a.N + NT * 16 - 1) / (NT * 16)), experts);
-    hipLaunchKernelGGL((expert_matvec_kernel<E4M3, MODE, NT, MT, WAVES>), grid, dim3(WAVES * kWave), 0, stream, a);
-    return hipGetLastError();
+    const int64_t experts = a.E < a.num_rows ? a.E : a.num_rows;
+    // no expert has more rows than there are; of many experts few have four times the average
+    if (a.num_rows <= 8 || a.num_rows <= 2 * a.E) return launch_rows<E4M3, MODE, 8>(a, experts, stream);
+    return launch_rows<E4M3, MODE, 32>(a, experts, stream);
 }
 
 }  // namespace
