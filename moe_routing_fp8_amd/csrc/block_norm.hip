@@ -25,8 +25,9 @@ namespace {
 
 constexpr int kMaxRowThreads = 1024;
 constexpr int kMaxHidden = MOE_BLOCK_NORM_MAX_HIDDEN;
-// Workgroups of the backward pass: two for each of the 256 compute units.
-constexpr int64_t kGradBlocks = 512;
+// Workgroups of the backward pass: as many as keep 16 waves on each of the 256
+// compute units, one to four; each leaves one row of partial sums.
+constexpr int64_t kComputeUnits = 256;
 
 // 1 / sqrt(v): the hardware's estimate and one Newton step, which brings it
 // to within 1 ulp (0 and infinity keep the estimate's value).
@@ -161,54 +162,99 @@ struct NormGradArgs {
     int num_params;
 };
 
+// A row's four arrays as loaded.
+template <typename TR, typename TA, int VEC, int VPT>
+struct GradRow {
+    typename TR::template Raw<VEC> grad_res_out[VPT], res_out[VPT];
+    typename TA::template Raw<VEC> grad_normed[VPT], y[VPT];
+    float pre_rstd, post_rstd, token_gate;
+};
+
+// HELD: the next row's loads are in flight while a row is worked on, and the
+// parameters stay in registers.  The workgroup's waves fill a compute unit at
+// hidden 7168, so nothing else would cover a row's loads; reading the three
+// parameters again for each row would add 86 KB from the caches to the 129 KB
+// of the row.  Without (rows of more than 8 values a thread): neither fits.
 template <typename TR, typename TA, int VEC, int VPT>
 __global__ __launch_bounds__(kMaxRowThreads) void block_norm_grad_kernel(NormGradArgs a) {
+    constexpr bool HELD = VEC * VPT <= 8;
     __shared__ float part[3][kMaxRowThreads / kWave];
     const int H = a.hidden;
     const float inv_h = 1.0f / static_cast<float>(H);
     const bool pre = a.grad_normed != nullptr, block = a.y != nullptr, post = a.post_weight != nullptr;
     const bool channel = a.gate_mode == MOE_GATE_CHANNEL;
     float sum_post[VPT][VEC], sum_gate[VPT][VEC], sum_pre[VPT][VEC];
+    float held_post[HELD ? VPT : 1][VEC], held_gate[HELD ? VPT : 1][VEC], held_pre[HELD ? VPT : 1][VEC];
+    auto load_params = [&](int e, float(&wp)[VEC], float(&wg)[VEC], float(&wn)[VEC]) {
 #pragma unroll
-    for (int j = 0; j < VPT; ++j)
+        for (int i = 0; i < VEC; ++i) {
+            wp[i] = wg[i] = 1.0f;
+            wn[i] = 0.0f;
+        }
+        if (post) F32::load<VEC>(a.post_weight, e, wp);
+        if (channel) F32::load<VEC>(a.gate, e, wg);
+        if (pre) F32::load<VEC>(a.pre_weight, e, wn);
+    };
+    auto load = [&](GradRow<TR, TA, VEC, VPT>& row, int64_t t) {
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+            const int e = (threadIdx.x + j * blockDim.x) * VEC;
+            if (e >= H) continue;
+            if (a.grad_res_out != nullptr) row.grad_res_out[j].load(a.grad_res_out, t * H + e);
+            if (pre) {
+                row.res_out[j].load(a.res_out, t * a.res_out_stride + e);
+                row.grad_normed[j].load(a.grad_normed, t * H + e);
+            }
+            if (block) row.y[j].load(a.y, t * a.y_stride + e);
+        }
+        row.pre_rstd = pre ? a.pre_rstd[t] : 0.0f;
+        row.post_rstd = post ? a.post_rstd[t] : 1.0f;
+        row.token_gate = a.gate_mode == MOE_GATE_TOKEN ? a.gate[t] : 1.0f;
+    };
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
 #pragma unroll
         for (int i = 0; i < VEC; ++i) sum_post[j][i] = sum_gate[j][i] = sum_pre[j][i] = 0.0f;
+        const int e = (threadIdx.x + j * blockDim.x) * VEC;
+        if constexpr (HELD)
+            if (e < H) load_params(e, held_post[j], held_gate[j], held_pre[j]);
+    }
+    GradRow<TR, TA, VEC, VPT> row;
+    load(row, blockIdx.x);
     for (int64_t t = blockIdx.x; t < a.num_tokens; t += gridDim.x) {
-        float d[VPT][VEC], yh[VPT][VEC];
+        float d[VPT][VEC], yh[VPT][VEC], xh[VPT][VEC], g[VPT][VEC];
+        const float pre_rstd = row.pre_rstd, post_rstd = row.post_rstd, token_gate = row.token_gate;
         float dot = 0.0f;
         // D = dr' + rstd * (g - xh * mean(g * xh)), g = dn * pre_weight
-        {
-            float xh[VPT][VEC], g[VPT][VEC];
-            const float rstd = pre ? a.pre_rstd[t] : 0.0f;
 #pragma unroll
-            for (int j = 0; j < VPT; ++j) {
-                const int e = (threadIdx.x + j * blockDim.x) * VEC;
+        for (int j = 0; j < VPT; ++j) {
+            const int e = (threadIdx.x + j * blockDim.x) * VEC;
 #pragma unroll
-                for (int i = 0; i < VEC; ++i) d[j][i] = yh[j][i] = xh[j][i] = g[j][i] = 0.0f;
-                if (e >= H) continue;
-                if (a.grad_res_out != nullptr) TR::template load<VEC>(a.grad_res_out, t * H + e, d[j]);
-                if (block) TA::template load<VEC>(a.y, t * a.y_stride + e, yh[j]);
-                if (pre) {
-                    float w[VEC];
-                    TR::template load<VEC>(a.res_out, t * a.res_out_stride + e, xh[j]);
-                    TA::template load<VEC>(a.grad_normed, t * H + e, g[j]);
-                    F32::load<VEC>(a.pre_weight, e, w);
+            for (int i = 0; i < VEC; ++i) d[j][i] = yh[j][i] = xh[j][i] = g[j][i] = 0.0f;
+            if (e >= H) continue;
+            if (a.grad_res_out != nullptr) row.grad_res_out[j].unpack(d[j]);
+            if (block) row.y[j].unpack(yh[j]);
+            if (pre) {
+                row.res_out[j].unpack(xh[j]);
+                row.grad_normed[j].unpack(g[j]);
+                float wn[VEC];
+                if constexpr (!HELD) F32::load<VEC>(a.pre_weight, e, wn);
 #pragma unroll
-                    for (int i = 0; i < VEC; ++i) {
-                        xh[j][i] *= rstd;
-                        sum_pre[j][i] += g[j][i] * xh[j][i];
-                        g[j][i] *= w[i];
-                        dot += g[j][i] * xh[j][i];
-                    }
+                for (int i = 0; i < VEC; ++i) {
+                    xh[j][i] *= pre_rstd;
+                    sum_pre[j][i] = __builtin_fmaf(g[j][i], xh[j][i], sum_pre[j][i]);
+                    g[j][i] *= HELD ? held_pre[HELD ? j : 0][i] : wn[i];
+                    dot = __builtin_fmaf(g[j][i], xh[j][i], dot);
                 }
             }
-            if (pre) {
-                const float mean = block_sum(dot, part[0]) * inv_h;
+        }
+        if (t + gridDim.x < a.num_tokens) load(row, t + gridDim.x);
+        if (pre) {
+            const float mean = block_sum(dot, part[0]) * inv_h;
 #pragma unroll
-                for (int j = 0; j < VPT; ++j)
+            for (int j = 0; j < VPT; ++j)
 #pragma unroll
-                    for (int i = 0; i < VEC; ++i) d[j][i] += rstd * (g[j][i] - xh[j][i] * mean);
-            }
+                for (int i = 0; i < VEC; ++i) d[j][i] += pre_rstd * (g[j][i] - xh[j][i] * mean);
         }
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
@@ -220,32 +266,26 @@ __global__ __launch_bounds__(kMaxRowThreads) void block_norm_grad_kernel(NormGra
             TR::template store<VEC>(a.grad_residual, t * H + e, o);
         }
         if (block) {
-            const float rstd = post ? a.post_rstd[t] : 1.0f;
-            const float token_gate = a.gate_mode == MOE_GATE_TOKEN ? a.gate[t] : 1.0f;
             float dot_gate = 0.0f;
             dot = 0.0f;
 #pragma unroll
             for (int j = 0; j < VPT; ++j) {
                 const int e = (threadIdx.x + j * blockDim.x) * VEC;
                 if (e >= H) continue;
-                float w[VEC], g[VEC];
+                float wp[VEC], wg[VEC], wn[VEC];
+                if constexpr (!HELD) load_params(e, wp, wg, wn);
 #pragma unroll
                 for (int i = 0; i < VEC; ++i) {
-                    w[i] = 1.0f;
-                    g[i] = token_gate;
-                }
-                if (post) F32::load<VEC>(a.post_weight, e, w);
-                if (channel) F32::load<VEC>(a.gate, e, g);
-#pragma unroll
-                for (int i = 0; i < VEC; ++i) {
-                    yh[j][i] *= rstd;
-                    const float along = d[j][i] * (yh[j][i] * w[i]);
+                    const float w = HELD ? held_post[HELD ? j : 0][i] : wp[i];
+                    const float gate = channel ? (HELD ? held_gate[HELD ? j : 0][i] : wg[i]) : token_gate;
+                    yh[j][i] *= post_rstd;
+                    const float along = d[j][i] * (yh[j][i] * w);
                     dot_gate += along;
                     sum_gate[j][i] += along;
-                    d[j][i] *= g[i];                      // du
-                    sum_post[j][i] += d[j][i] * yh[j][i];
-                    d[j][i] *= w[i];
-                    dot += d[j][i] * yh[j][i];
+                    d[j][i] *= gate;  // du
+                    sum_post[j][i] = __builtin_fmaf(d[j][i], yh[j][i], sum_post[j][i]);
+                    d[j][i] *= w;
+                    dot = __builtin_fmaf(d[j][i], yh[j][i], dot);
                 }
             }
             if (a.gate_mode == MOE_GATE_TOKEN) {
@@ -257,7 +297,7 @@ __global__ __launch_bounds__(kMaxRowThreads) void block_norm_grad_kernel(NormGra
 #pragma unroll
                 for (int j = 0; j < VPT; ++j)
 #pragma unroll
-                    for (int i = 0; i < VEC; ++i) d[j][i] = rstd * (d[j][i] - yh[j][i] * mean);
+                    for (int i = 0; i < VEC; ++i) d[j][i] = post_rstd * (d[j][i] - yh[j][i] * mean);
             }
 #pragma unroll
             for (int j = 0; j < VPT; ++j) {
@@ -285,9 +325,9 @@ __global__ __launch_bounds__(kMaxRowThreads) void block_norm_grad_kernel(NormGra
     }
 }
 
-// The parameters' gradients: column sums of the workgroups' partials, rows in
-// order within each of kSumWaves waves, then the waves in order.
-constexpr int kSumWaves = 8;
+// The parameters' gradients: column sums of the workgroups' partials, each of
+// kSumWaves waves every kSumWaves-th row in order, then the waves in order.
+constexpr int kSumWaves = 16;
 __global__ __launch_bounds__(kSumWaves* kWave) void block_norm_param_kernel(const float* __restrict__ partials,
                                                                              int64_t blocks, int width, int H,
                                                                              float* o0, float* o1, float* o2) {
@@ -296,6 +336,7 @@ __global__ __launch_bounds__(kSumWaves* kWave) void block_norm_param_kernel(cons
     const int c = blockIdx.x * kWave + lane;
     float v = 0.0f;
     if (c < width)
+#pragma unroll 8
         for (int64_t b = wave; b < blocks; b += kSumWaves) v += partials[b * width + c];
     lds[wave][lane] = v;
     __syncthreads();
@@ -363,7 +404,11 @@ bool vec_rows(const void* p, int64_t stride, int32_t dtype) {
     return aligned(p, 16) && stride * dtype_bytes(dtype) % 16 == 0;
 }
 
-int64_t grad_blocks(int64_t T) { return T < kGradBlocks ? T : kGradBlocks; }
+int64_t grad_blocks(int64_t T, int H) {
+    const int waves = row_threads(H, 8, 1) / kWave;
+    const int64_t most = kComputeUnits * (waves > 8 ? 1 : waves > 4 ? 2 : 4);
+    return T < most ? T : most;
+}
 
 }  // namespace
 }  // namespace moe
@@ -413,7 +458,7 @@ moe_status moe_block_norm(const void* residual, int64_t residual_stride, int32_t
 
 size_t moe_block_norm_backward_workspace_bytes(int64_t num_tokens, int32_t hidden) {
     if (num_tokens < 0 || num_tokens > MOE_BLOCK_NORM_MAX_TOKENS || hidden < 1 || hidden > moe::kMaxHidden) return 0;
-    const size_t n = static_cast<size_t>(moe::grad_blocks(num_tokens)) * 3 * static_cast<size_t>(hidden) * 4;
+    const size_t n = static_cast<size_t>(moe::grad_blocks(num_tokens, hidden)) * 3 * static_cast<size_t>(hidden) * 4;
     return (n + 255) / 256 * 256;
 }
 
@@ -467,7 +512,7 @@ moe_status moe_block_norm_backward(const void* grad_res_out, const void* grad_no
         if (workspace_bytes < moe_block_norm_backward_workspace_bytes(num_tokens, hidden))
             return MOE_ERR_WORKSPACE_TOO_SMALL;
     }
-    const int64_t blocks = grad_blocks(num_tokens);
+    const int64_t blocks = grad_blocks(num_tokens, hidden);
     float* partials = static_cast<float*>(workspace);
     if (num_tokens > 0) {
         const bool vec = hidden % 8 == 0 && aligned(grad_res_out, 16) && aligned(grad_normed, 16) &&

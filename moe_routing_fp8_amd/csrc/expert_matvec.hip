@@ -44,7 +44,7 @@ typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
 typedef float f32x4_t __attribute__((ext_vector_type(4)));
 
 constexpr int kStep = 128;  // k per step of a wave
-constexpr int kMaxSplit = 8;  // waves that share a tile's k range
+constexpr int kMaxSplit = 4;  // waves that share a tile's k range
 constexpr int kMaxThreads = kMaxSplit * kWave;
 enum ScaleMode { kFolded = 0, kF32Group128 = 1, kF32Group32 = 2 };
 
@@ -242,9 +242,23 @@ __device__ __forceinline__ void multiply_rows(const MatvecArgs& a, const Share& 
             xsp[mt] = r < 0 ? nullptr : a.x_sf + r * (K / 128);
         }
 
-    auto multiply = [&](const u32x4_t(&w)[kNT], const float(&ws)[kNT][4], const u32x4_t(&x)[MT][XV],
-                        const float(&xs_own)[MT]) __attribute__((always_inline)) {
-        bf16x8_t wf[kNT][4];
+    auto unpack_x = [&](bf16x8_t(&xf)[4], const u32x4_t(&x)[XV]) __attribute__((always_inline)) {
+        if constexpr (E4M3) {
+            xf[0] = e4m3_to_bf16(x[0].x, x[0].y);
+            xf[1] = e4m3_to_bf16(x[0].z, x[0].w);
+            xf[2] = e4m3_to_bf16(x[1].x, x[1].y);
+            xf[3] = e4m3_to_bf16(x[1].z, x[1].w);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                Frag f;
+                f.u = x[i];
+                xf[i] = f.v;
+            }
+        }
+    };
+    auto unpack_codes = [&](bf16x8_t(&wf)[kNT][4], const u32x4_t(&w)[kNT], const float(&ws)[kNT][4])
+        __attribute__((always_inline)) {
 #pragma unroll
         for (int nt = 0; nt < kNT; ++nt) {
             uint32_t d[4] = {w[nt].x, w[nt].y, w[nt].z, w[nt].w};
@@ -252,58 +266,45 @@ __device__ __forceinline__ void multiply_rows(const MatvecArgs& a, const Share& 
 #pragma unroll
             for (int i = 0; i < 4; ++i) wf[nt][i] = e2m1_to_bf16(d[i], MODE == kFolded ? ws[nt][0] : 1.0f);
         }
+    };
+    // Sums of 16 rows from their fragments; xs_own: the scale of the lane's e4m3 row.
+    auto multiply = [&](const bf16x8_t(&wf)[kNT][4], const float(&ws)[kNT][4], const u32x4_t(&x)[XV], float xs_own,
+                        f32x4_t(&sum)[kNT]) __attribute__((always_inline)) {
+        bf16x8_t xf[4];
+        unpack_x(xf, x);
+        float xs[4] = {1.0f, 1.0f, 1.0f, 1.0f};  // kXFirst: of the lane's four sums' rows; else [0]
+        if constexpr (E4M3) {
+            xs[0] = xs_own;
+            if constexpr (kXFirst) {
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-            bf16x8_t xf[4];
-            if constexpr (E4M3) {
-                xf[0] = e4m3_to_bf16(x[mt][0].x, x[mt][0].y);
-                xf[1] = e4m3_to_bf16(x[mt][0].z, x[mt][0].w);
-                xf[2] = e4m3_to_bf16(x[mt][1].x, x[mt][1].y);
-                xf[3] = e4m3_to_bf16(x[mt][1].z, x[mt][1].w);
+                for (int j = 0; j < 4; ++j) xs[j] = __shfl(xs_own, q * 4 + j, kWave);
+            }
+        }
+#pragma unroll
+        for (int nt = 0; nt < kNT; ++nt) {
+            if constexpr (MODE == kFolded) {
+                f32x4_t d = E4M3 ? f32x4_t{0.0f, 0.0f, 0.0f, 0.0f} : sum[nt];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wf[nt][i], xf[i], d, 0, 0, 0);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) sum[nt][j] = E4M3 ? __builtin_fmaf(xs[0], d[j], sum[nt][j]) : d[j];
+            } else if constexpr (MODE == kF32Group128) {
+                f32x4_t d = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf[i], wf[nt][i], d, 0, 0, 0);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) sum[nt][j] = __builtin_fmaf(ws[nt][0] * xs[j], d[j], sum[nt][j]);
             } else {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    Frag f;
-                    f.u = x[mt][i];
-                    xf[i] = f.v;
-                }
-            }
-            float xs[4] = {1.0f, 1.0f, 1.0f, 1.0f};  // kXFirst: of the lane's four sums' rows; else [0]
-            if constexpr (E4M3) {
-                xs[0] = xs_own[mt];
-                if constexpr (kXFirst) {
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) xs[j] = __shfl(xs_own[mt], q * 4 + j, kWave);
-                }
-            }
-#pragma unroll
-            for (int nt = 0; nt < kNT; ++nt) {
-                if constexpr (MODE == kFolded) {
-                    f32x4_t d = E4M3 ? f32x4_t{0.0f, 0.0f, 0.0f, 0.0f} : acc[mt][nt];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wf[nt][i], xf[i], d, 0, 0, 0);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        acc[mt][nt][j] = E4M3 ? __builtin_fmaf(xs[0], d[j], acc[mt][nt][j]) : d[j];
-                } else if constexpr (MODE == kF32Group128) {
                     f32x4_t d = {0.0f, 0.0f, 0.0f, 0.0f};
+                    d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf[i], wf[nt][i], d, 0, 0, 0);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf[i], wf[nt][i], d, 0, 0, 0);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        acc[mt][nt][j] = __builtin_fmaf(ws[nt][0] * xs[j], d[j], acc[mt][nt][j]);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        f32x4_t d = {0.0f, 0.0f, 0.0f, 0.0f};
-                        d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf[i], wf[nt][i], d, 0, 0, 0);
-#pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            acc[mt][nt][j] = __builtin_fmaf(ws[nt][i] * xs[j], d[j], acc[mt][nt][j]);
-                    }
+                    for (int j = 0; j < 4; ++j) sum[nt][j] = __builtin_fmaf(ws[nt][i] * xs[j], d[j], sum[nt][j]);
                 }
+                __builtin_amdgcn_sched_barrier(0);
             }
         }
     };
@@ -394,8 +395,8 @@ __device__ __forceinline__ void multiply_rows(const MatvecArgs& a, const Share& 
                     if (j % kPair == 0) load_codes(w[j / kPair], step + kBlock + j);
                 }
                 wave_lds_order();
-                u32x4_t wl[kNT], xl[MT][XV];
-                float ws[kNT][4], xs_step[MT];
+                u32x4_t wl[kNT];
+                float ws[kNT][4];
 #pragma unroll
                 for (int nt = 0; nt < kNT; ++nt) {
                     wl[nt] = lds_w[nt * (kPair * kWave) + lr * 8 + ((j % kPair * 4 + q) ^ (lr & 7))];
@@ -413,27 +414,31 @@ __device__ __forceinline__ void multiply_rows(const MatvecArgs& a, const Share& 
                         ws[nt][3] = __uint_as_float(v.w);
                     }
                 }
+                bf16x8_t wf[kNT][4];
+                unpack_codes(wf, wl, ws);
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt) {
                     const int m = mt * 16 + lr;
                     const u32x4_t* row = x_lds + (SHARED ? j * kStepX : 0) + m * kChunks;
+                    u32x4_t xl[XV];
                     if constexpr (MODE == kF32Group32 && E4M3) {  // k = 32 i + 8 q of instruction i: half a chunk
                         u32x2_t c[4];
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
                             c[i] = reinterpret_cast<const u32x2_t*>(row + ((2 * i + (q >> 1)) ^ (m & 7)))[q & 1];
-                        xl[mt][0] = u32x4(c[0].x, c[0].y, c[1].x, c[1].y);
-                        xl[mt][1] = u32x4(c[2].x, c[2].y, c[3].x, c[3].y);
+                        xl[0] = u32x4(c[0].x, c[0].y, c[1].x, c[1].y);
+                        xl[1] = u32x4(c[2].x, c[2].y, c[3].x, c[3].y);
                     } else {
 #pragma unroll
                         for (int i = 0; i < XV; ++i)
-                            xl[mt][i] = row[(MODE == kF32Group32 ? 4 * i + q : XV * q + i) ^ (m & (kChunks - 1))];
+                            xl[i] = row[(MODE == kF32Group32 ? 4 * i + q : XV * q + i) ^ (m & (kChunks - 1))];
                     }
-                    xs_step[mt] = j == 0 ? xs[mt].x : j == 1 ? xs[mt].y : j == 2 ? xs[mt].z : xs[mt].w;
+                    const float own = j == 0 ? xs[mt].x : j == 1 ? xs[mt].y : j == 2 ? xs[mt].z : xs[mt].w;
+                    multiply(wf, ws, xl, own, acc[mt]);
+                    // the next rows' (or step's) fragments would not fit the registers as well
+                    __builtin_amdgcn_sched_barrier(0);
                 }
                 wave_lds_order();
-                multiply(wl, ws, xl, xs_step);
-                __builtin_amdgcn_sched_barrier(0);  // the next step's fragments would not fit the registers as well
             }
         }
     }
@@ -492,7 +497,10 @@ __device__ __forceinline__ void multiply_rows(const MatvecArgs& a, const Share& 
                 }
             }
         }
-        multiply(w, ws, x, xs);
+        bf16x8_t wf[kNT][4];
+        unpack_codes(wf, w, ws);
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) multiply(wf, ws, x[mt], xs[mt], acc[mt]);
     }
 }
 
@@ -501,7 +509,7 @@ __device__ __forceinline__ void multiply_rows(const MatvecArgs& a, const Share& 
 // rows that one pass over the weights serves; an expert with more takes
 // several.
 template <bool E4M3, int MODE, int MAXROWS, bool SHARED>
-__global__ __launch_bounds__(kMaxThreads) void expert_matvec_kernel(MatvecArgs a) {
+__global__ __launch_bounds__(kMaxThreads, 2) void expert_matvec_kernel(MatvecArgs a) {
     // the operand whose scale is per row of its own goes second: a lane's four
     // sums then share that row
     constexpr bool kXFirst = MODE != kFolded;
@@ -574,7 +582,7 @@ __global__ __launch_bounds__(kMaxThreads) void expert_matvec_kernel(MatvecArgs a
             run(std::integral_constant<int, 4>{}, m0);
         else if (MAXROWS <= 8 || rows <= 8)
             run(std::integral_constant<int, 8>{}, m0);
-        else if (rows <= 16)
+        else if (MAXROWS <= 16 || rows <= 16)
             run(std::integral_constant<int, MAXROWS < 16 ? MAXROWS : 16>{}, m0);
         else
             run(std::integral_constant<int, MAXROWS>{}, m0);
@@ -607,7 +615,8 @@ hipError_t launch_matvec(const MatvecArgs& a, hipStream_t stream) {
     const int64_t experts = a.E < a.num_rows ? a.E : a.num_rows;
     // no expert has more rows than there are; of many experts few have four times the average
     if (a.num_rows <= 8 || a.num_rows <= 2 * a.E) return launch_rows<E4M3, MODE, 8>(a, experts, stream);
-    return launch_rows<E4M3, MODE, 32>(a, experts, stream);
+    // fp32 scales of 32 channels take registers for four sums at a time: 32 rows of them do not fit
+    return launch_rows<E4M3, MODE, MODE == kF32Group32 ? 16 : 32>(a, experts, stream);
 }
 
 }  // namespace

@@ -2,6 +2,8 @@
 // balance loss kernels.
 #pragma once
 
+#include <type_traits>
+
 #include "device_utils.hpp"
 
 namespace moe {
@@ -80,8 +82,29 @@ __device__ __forceinline__ uint32_t bf16_pack2(float lo, float hi) {
 // Element types of the operators that take bf16 or fp32: VEC consecutive
 // values to and from fp32 registers.  VEC > 1 needs the address aligned to
 // min(16, VEC * sizeof(T)) bytes.
+//
+// Raw<VEC>: the values as loaded, to be unpacked later.
 struct Bf16 {
     static constexpr int kBytes = 2;
+    template <int VEC>
+    struct Raw {
+        static_assert(VEC == 8 || VEC == 1, "vector width");
+        typename std::conditional<VEC == 8, u32x4_t, uint16_t>::type v;
+        __device__ __forceinline__ void load(const void* p, int64_t i) {
+            v = *reinterpret_cast<const decltype(v)*>(static_cast<const uint16_t*>(p) + i);
+        }
+        __device__ __forceinline__ void unpack(float (&f)[VEC]) const {
+            if constexpr (VEC == 8) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    f[2 * k] = bf16_lo(v[k]);
+                    f[2 * k + 1] = bf16_hi(v[k]);
+                }
+            } else {
+                f[0] = __uint_as_float(static_cast<uint32_t>(v) << 16);
+            }
+        }
+    };
     template <int VEC>
     static __device__ __forceinline__ void load(const void* p, int64_t i, float (&f)[VEC]) {
         const uint16_t* q = static_cast<const uint16_t*>(p) + i;
@@ -123,6 +146,25 @@ struct Bf16 {
 
 struct F32 {
     static constexpr int kBytes = 4;
+    template <int VEC>
+    struct Raw {
+        static_assert(VEC == 8 || VEC == 1, "vector width");
+        static constexpr int N = VEC == 8 ? 2 : 1;
+        typename std::conditional<VEC == 8, u32x4_t, uint32_t>::type v[N];
+        __device__ __forceinline__ void load(const void* p, int64_t i) {
+#pragma unroll
+            for (int n = 0; n < N; ++n)
+                v[n] = reinterpret_cast<const std::remove_reference_t<decltype(v[0])>*>(static_cast<const float*>(p) + i)[n];
+        }
+        __device__ __forceinline__ void unpack(float (&f)[VEC]) const {
+            if constexpr (VEC == 8) {
+#pragma unroll
+                for (int k = 0; k < 8; ++k) f[k] = __uint_as_float(v[k / 4][k % 4]);
+            } else {
+                f[0] = __uint_as_float(v[0]);
+            }
+        }
+    };
     template <int VEC>
     static __device__ __forceinline__ void load(const void* p, int64_t i, float (&f)[VEC]) {
         const float* q = static_cast<const float*>(p) + i;
