@@ -38,9 +38,15 @@ __device__ __forceinline__ float rsqrt_f32(float v) {
     return v > 0.0f && v < INFINITY ? n : r;
 }
 
-// Sum over the workgroup, in a fixed order; every thread receives it.
-// `part` holds one float per wave; the caller alternates between two of them
-// so that one barrier per sum is enough.
+// Rows of more bytes than this in all are read and written past the caches
+// (half of the 256 MB of Infinity Cache: what is larger finds nothing there
+// when it comes round again).  4096 x 7168 bf16: 48.0 us against 54.8.  The
+// backward pass streams its stores only (119.1 us against 121.8; with
+// streaming loads 131).
+constexpr int64_t kStreamBytes = int64_t{128} << 20;
+
+// Sum over the workgroup, in a fixed order; every thread receives it.  `part`
+// holds one float per wave and is not written again before another barrier.
 __device__ __forceinline__ float block_sum(float v, float* part) {
     v = wave_sum_f32(v);
     const int waves = blockDim.x / kWave;
@@ -73,7 +79,7 @@ struct NormArgs {
 
 // Thread i's j-th vector of a row starts at element (i + j * blockDim.x) * VEC.
 // VEC == 8 needs 16-byte aligned rows and H % 8 == 0; VEC == 1 takes any.
-template <typename TR, typename TA, int VEC, int VPT>
+template <typename TR, typename TA, int VEC, int VPT, bool STREAM>
 __global__ __launch_bounds__(kMaxRowThreads) void block_norm_kernel(NormArgs a) {
     __shared__ float part[2][kMaxRowThreads / kWave];
     const int64_t t = blockIdx.x;
@@ -87,8 +93,8 @@ __global__ __launch_bounds__(kMaxRowThreads) void block_norm_kernel(NormArgs a) 
 #pragma unroll
         for (int i = 0; i < VEC; ++i) r[j][i] = u[j][i] = 0.0f;
         if (e < H) {
-            TR::template load<VEC>(a.residual, t * a.residual_stride + e, r[j]);
-            if (a.y != nullptr) TA::template load<VEC>(a.y, t * a.y_stride + e, u[j]);
+            TR::template load<VEC, STREAM>(a.residual, t * a.residual_stride + e, r[j]);
+            if (a.y != nullptr) TA::template load<VEC, STREAM>(a.y, t * a.y_stride + e, u[j]);
         }
     }
     if (a.y != nullptr) {
@@ -116,7 +122,7 @@ __global__ __launch_bounds__(kMaxRowThreads) void block_norm_kernel(NormArgs a) 
             if (a.gate_mode == MOE_GATE_CHANNEL) F32::load<VEC>(a.gate, e, g);
 #pragma unroll
             for (int i = 0; i < VEC; ++i) r[j][i] = a.residual_scale * r[j][i] + g[i] * (u[j][i] * rstd * w[i]);
-            TR::template store<VEC>(a.res_out, t * H + e, r[j]);
+            TR::template store<VEC, STREAM>(a.res_out, t * H + e, r[j]);
         }
     }
     if (a.normed == nullptr) return;
@@ -135,7 +141,7 @@ __global__ __launch_bounds__(kMaxRowThreads) void block_norm_kernel(NormArgs a) 
         F32::load<VEC>(a.pre_weight, e, w);
 #pragma unroll
         for (int i = 0; i < VEC; ++i) w[i] = r[j][i] * rstd * w[i];
-        TA::template store<VEC>(a.normed, t * H + e, w);
+        TA::template store<VEC, STREAM>(a.normed, t * H + e, w);
     }
 }
 
@@ -175,10 +181,12 @@ struct GradRow {
 // hidden 7168, so nothing else would cover a row's loads; reading the three
 // parameters again for each row would add 86 KB from the caches to the 129 KB
 // of the row.  Without (rows of more than 8 values a thread): neither fits.
-template <typename TR, typename TA, int VEC, int VPT>
+template <typename TR, typename TA, int VEC, int VPT, bool STREAM>
 __global__ __launch_bounds__(kMaxRowThreads) void block_norm_grad_kernel(NormGradArgs a) {
     constexpr bool HELD = VEC * VPT <= 8;
-    __shared__ float part[3][kMaxRowThreads / kWave];
+    // two sets in turn: a row's sums have been read before the next row but one writes there
+    __shared__ float part[2][3][kMaxRowThreads / kWave];
+    int turn = 0;
     const int H = a.hidden;
     const float inv_h = 1.0f / static_cast<float>(H);
     const bool pre = a.grad_normed != nullptr, block = a.y != nullptr, post = a.post_weight != nullptr;
@@ -220,8 +228,9 @@ __global__ __launch_bounds__(kMaxRowThreads) void block_norm_grad_kernel(NormGra
             if (e < H) load_params(e, held_post[j], held_gate[j], held_pre[j]);
     }
     GradRow<TR, TA, VEC, VPT> row;
-    load(row, blockIdx.x);
-    for (int64_t t = blockIdx.x; t < a.num_tokens; t += gridDim.x) {
+    if constexpr (HELD) load(row, blockIdx.x);
+    for (int64_t t = blockIdx.x; t < a.num_tokens; t += gridDim.x, turn ^= 1) {
+        if constexpr (!HELD) load(row, t);
         float d[VPT][VEC], yh[VPT][VEC], xh[VPT][VEC], g[VPT][VEC];
         const float pre_rstd = row.pre_rstd, post_rstd = row.post_rstd, token_gate = row.token_gate;
         float dot = 0.0f;
@@ -248,9 +257,10 @@ __global__ __launch_bounds__(kMaxRowThreads) void block_norm_grad_kernel(NormGra
                 }
             }
         }
-        if (t + gridDim.x < a.num_tokens) load(row, t + gridDim.x);
+        if constexpr (HELD)
+            if (t + gridDim.x < a.num_tokens) load(row, t + gridDim.x);
         if (pre) {
-            const float mean = block_sum(dot, part[0]) * inv_h;
+            const float mean = block_sum(dot, part[turn][0]) * inv_h;
 #pragma unroll
             for (int j = 0; j < VPT; ++j)
 #pragma unroll
@@ -263,7 +273,7 @@ __global__ __launch_bounds__(kMaxRowThreads) void block_norm_grad_kernel(NormGra
             float o[VEC];
 #pragma unroll
             for (int i = 0; i < VEC; ++i) o[i] = a.residual_scale * d[j][i];
-            TR::template store<VEC>(a.grad_residual, t * H + e, o);
+            TR::template store<VEC, STREAM>(a.grad_residual, t * H + e, o);
         }
         if (block) {
             float dot_gate = 0.0f;
@@ -289,11 +299,11 @@ __global__ __launch_bounds__(kMaxRowThreads) void block_norm_grad_kernel(NormGra
                 }
             }
             if (a.gate_mode == MOE_GATE_TOKEN) {
-                dot_gate = block_sum(dot_gate, part[1]);
+                dot_gate = block_sum(dot_gate, part[turn][1]);
                 if (threadIdx.x == 0) a.grad_token_gate[t] = dot_gate;
             }
             if (post) {
-                const float mean = block_sum(dot, part[2]) * inv_h;
+                const float mean = block_sum(dot, part[turn][2]) * inv_h;
 #pragma unroll
                 for (int j = 0; j < VPT; ++j)
 #pragma unroll
@@ -302,10 +312,9 @@ __global__ __launch_bounds__(kMaxRowThreads) void block_norm_grad_kernel(NormGra
 #pragma unroll
             for (int j = 0; j < VPT; ++j) {
                 const int e = (threadIdx.x + j * blockDim.x) * VEC;
-                if (e < H) TA::template store<VEC>(a.grad_y, t * H + e, d[j]);
+                if (e < H) TA::template store<VEC, STREAM>(a.grad_y, t * H + e, d[j]);
             }
         }
-        __syncthreads();  // the sums' exchange is written again by the next row
     }
     float* out = a.partials + static_cast<int64_t>(blockIdx.x) * a.num_params * H;
 #pragma unroll
@@ -363,31 +372,40 @@ int row_threads(int H, int vec, int vpt) {
     return (n + kWave - 1) / kWave * kWave;
 }
 
-template <typename TR, typename TA, int VEC, int VPT>
+template <typename TR, typename TA, int VEC, int VPT, bool STREAM>
 hipError_t launch_norm(const NormArgs& a, hipStream_t stream) {
-    hipLaunchKernelGGL((block_norm_kernel<TR, TA, VEC, VPT>), dim3(static_cast<unsigned>(a.num_tokens)),
+    hipLaunchKernelGGL((block_norm_kernel<TR, TA, VEC, VPT, STREAM>), dim3(static_cast<unsigned>(a.num_tokens)),
                        dim3(row_threads(a.hidden, VEC, VPT)), 0, stream, a);
     return hipGetLastError();
 }
+// Two vectors a thread where the rows fill the chip (their shorter workgroups
+// overlap: 48.0 us against 50.8 with one) or do not fit otherwise; one where
+// the latency of a few rows counts.
 template <typename TR, typename TA>
-hipError_t launch_norm_types(const NormArgs& a, bool vec, hipStream_t stream) {
-    if (vec) return a.hidden <= 8 * kMaxRowThreads ? launch_norm<TR, TA, 8, 1>(a, stream) : launch_norm<TR, TA, 8, 2>(a, stream);
-    return a.hidden <= 4 * kMaxRowThreads ? launch_norm<TR, TA, 1, 4>(a, stream) : launch_norm<TR, TA, 1, 16>(a, stream);
+hipError_t launch_norm_types(const NormArgs& a, bool vec, bool far, hipStream_t stream) {
+    if (!vec)
+        return a.hidden <= 4 * kMaxRowThreads ? launch_norm<TR, TA, 1, 4, false>(a, stream)
+                                              : launch_norm<TR, TA, 1, 16, false>(a, stream);
+    if (far) return launch_norm<TR, TA, 8, 2, true>(a, stream);
+    if (a.hidden <= 8 * kMaxRowThreads && a.num_tokens <= 2 * kComputeUnits)
+        return launch_norm<TR, TA, 8, 1, false>(a, stream);
+    return launch_norm<TR, TA, 8, 2, false>(a, stream);
 }
 
-template <typename TR, typename TA, int VEC, int VPT>
+template <typename TR, typename TA, int VEC, int VPT, bool STREAM>
 hipError_t launch_grad(const NormGradArgs& a, int64_t blocks, hipStream_t stream) {
-    hipLaunchKernelGGL((block_norm_grad_kernel<TR, TA, VEC, VPT>), dim3(static_cast<unsigned>(blocks)),
+    hipLaunchKernelGGL((block_norm_grad_kernel<TR, TA, VEC, VPT, STREAM>), dim3(static_cast<unsigned>(blocks)),
                        dim3(row_threads(a.hidden, VEC, VPT)), 0, stream, a);
     return hipGetLastError();
 }
 template <typename TR, typename TA>
-hipError_t launch_grad_types(const NormGradArgs& a, int64_t blocks, bool vec, hipStream_t stream) {
-    if (vec)
-        return a.hidden <= 8 * kMaxRowThreads ? launch_grad<TR, TA, 8, 1>(a, blocks, stream)
-                                              : launch_grad<TR, TA, 8, 2>(a, blocks, stream);
-    return a.hidden <= 4 * kMaxRowThreads ? launch_grad<TR, TA, 1, 4>(a, blocks, stream)
-                                          : launch_grad<TR, TA, 1, 16>(a, blocks, stream);
+hipError_t launch_grad_types(const NormGradArgs& a, int64_t blocks, bool vec, bool far, hipStream_t stream) {
+    if (!vec)
+        return a.hidden <= 4 * kMaxRowThreads ? launch_grad<TR, TA, 1, 4, false>(a, blocks, stream)
+                                              : launch_grad<TR, TA, 1, 16, false>(a, blocks, stream);
+    if (a.hidden > 8 * kMaxRowThreads) return launch_grad<TR, TA, 8, 2, false>(a, blocks, stream);
+    return far ? launch_grad<TR, TA, 8, 1, true>(a, blocks, stream)
+               : launch_grad<TR, TA, 8, 1, false>(a, blocks, stream);
 }
 
 // Calls f with the two element types.
@@ -451,8 +469,10 @@ moe_status moe_block_norm(const void* residual, int64_t residual_stride, int32_t
                      (gate_mode != MOE_GATE_CHANNEL || aligned(gate, 16));
     const NormArgs a{residual,  residual_stride, y,          y_stride, num_tokens, hidden, post_weight, gate,
                      gate_mode, residual_scale,  pre_weight, eps,      res_out,    normed, post_rstd,   pre_rstd};
+    const int64_t row_bytes = int64_t{2} * hidden * (rb + ab);
+    const bool far = num_tokens * row_bytes > kStreamBytes;
     return hip_status(with_types(residual_dtype, act_dtype, [&](auto r, auto x) {
-        return launch_norm_types<decltype(r), decltype(x)>(a, vec, stream);
+        return launch_norm_types<decltype(r), decltype(x)>(a, vec, far, stream);
     }));
 }
 
@@ -540,8 +560,9 @@ moe_status moe_block_norm_backward(const void* grad_res_out, const void* grad_no
                              gate_mode == MOE_GATE_TOKEN ? grad_gate : nullptr,
                              partials,
                              params};
+        const bool far = num_tokens * (int64_t{3} * hidden * (rb + ab)) > kStreamBytes;
         const hipError_t err = with_types(residual_dtype, act_dtype, [&](auto r, auto x) {
-            return launch_grad_types<decltype(r), decltype(x)>(a, blocks, vec, stream);
+            return launch_grad_types<decltype(r), decltype(x)>(a, blocks, vec, far, stream);
         });
         if (err != hipSuccess) return hip_status(err);
     }

@@ -79,9 +79,22 @@ __device__ __forceinline__ uint32_t bf16_pack2(float lo, float hi) {
     return static_cast<uint32_t>(bf16_bits(lo)) | (static_cast<uint32_t>(bf16_bits(hi)) << 16);
 }
 
+template <bool STREAM>
+__device__ __forceinline__ uint4 load16(const uint4* p) {
+    if constexpr (STREAM) return load_stream16(p);
+    return *p;
+}
+template <bool STREAM>
+__device__ __forceinline__ void store16(uint4* p, const uint4& v) {
+    if constexpr (STREAM)
+        store_stream16(p, v);
+    else
+        *p = v;
+}
+
 // Element types of the operators that take bf16 or fp32: VEC consecutive
 // values to and from fp32 registers.  VEC > 1 needs the address aligned to
-// min(16, VEC * sizeof(T)) bytes.
+// min(16, VEC * sizeof(T)) bytes.  STREAM: non-temporal 16-byte accesses.
 //
 // Raw<VEC>: the values as loaded, to be unpacked later.
 struct Bf16 {
@@ -105,13 +118,14 @@ struct Bf16 {
             }
         }
     };
-    template <int VEC>
+    template <int VEC, bool STREAM = false>
     static __device__ __forceinline__ void load(const void* p, int64_t i, float (&f)[VEC]) {
         const uint16_t* q = static_cast<const uint16_t*>(p) + i;
         if constexpr (VEC % 8 == 0) {
 #pragma unroll
             for (int v = 0; v < VEC / 8; ++v)
-                unpack8_bf16(reinterpret_cast<const uint4*>(q)[v], *reinterpret_cast<float(*)[8]>(f + 8 * v));
+                unpack8_bf16(load16<STREAM>(reinterpret_cast<const uint4*>(q) + v),
+                             *reinterpret_cast<float(*)[8]>(f + 8 * v));
         } else if constexpr (VEC == 4) {
             const uint2 r = *reinterpret_cast<const uint2*>(q);
             f[0] = bf16_lo(r.x); f[1] = bf16_hi(r.x); f[2] = bf16_lo(r.y); f[3] = bf16_hi(r.y);
@@ -123,15 +137,16 @@ struct Bf16 {
             f[0] = __uint_as_float(static_cast<uint32_t>(*q) << 16);
         }
     }
-    template <int VEC>
+    template <int VEC, bool STREAM = false>
     static __device__ __forceinline__ void store(void* p, int64_t i, const float (&f)[VEC]) {
         uint16_t* q = static_cast<uint16_t*>(p) + i;
         if constexpr (VEC % 8 == 0) {
 #pragma unroll
             for (int v = 0; v < VEC / 8; ++v) {
                 const float* g = f + 8 * v;
-                reinterpret_cast<uint4*>(q)[v] = make_uint4(bf16_pack2(g[0], g[1]), bf16_pack2(g[2], g[3]),
-                                                            bf16_pack2(g[4], g[5]), bf16_pack2(g[6], g[7]));
+                store16<STREAM>(reinterpret_cast<uint4*>(q) + v,
+                                make_uint4(bf16_pack2(g[0], g[1]), bf16_pack2(g[2], g[3]), bf16_pack2(g[4], g[5]),
+                                           bf16_pack2(g[6], g[7])));
             }
         } else if constexpr (VEC == 4) {
             *reinterpret_cast<uint2*>(q) = make_uint2(bf16_pack2(f[0], f[1]), bf16_pack2(f[2], f[3]));
@@ -165,14 +180,15 @@ struct F32 {
             }
         }
     };
-    template <int VEC>
+    template <int VEC, bool STREAM = false>
     static __device__ __forceinline__ void load(const void* p, int64_t i, float (&f)[VEC]) {
         const float* q = static_cast<const float*>(p) + i;
         if constexpr (VEC % 4 == 0) {
 #pragma unroll
             for (int v = 0; v < VEC / 4; ++v) {
-                const float4 r = reinterpret_cast<const float4*>(q)[v];
-                f[4 * v] = r.x; f[4 * v + 1] = r.y; f[4 * v + 2] = r.z; f[4 * v + 3] = r.w;
+                const uint4 r = load16<STREAM>(reinterpret_cast<const uint4*>(q) + v);
+                f[4 * v] = __uint_as_float(r.x); f[4 * v + 1] = __uint_as_float(r.y);
+                f[4 * v + 2] = __uint_as_float(r.z); f[4 * v + 3] = __uint_as_float(r.w);
             }
         } else if constexpr (VEC == 2) {
             const float2 r = *reinterpret_cast<const float2*>(q);
@@ -182,13 +198,15 @@ struct F32 {
             f[0] = *q;
         }
     }
-    template <int VEC>
+    template <int VEC, bool STREAM = false>
     static __device__ __forceinline__ void store(void* p, int64_t i, const float (&f)[VEC]) {
         float* q = static_cast<float*>(p) + i;
         if constexpr (VEC % 4 == 0) {
 #pragma unroll
             for (int v = 0; v < VEC / 4; ++v)
-                reinterpret_cast<float4*>(q)[v] = make_float4(f[4 * v], f[4 * v + 1], f[4 * v + 2], f[4 * v + 3]);
+                store16<STREAM>(reinterpret_cast<uint4*>(q) + v,
+                                make_uint4(__float_as_uint(f[4 * v]), __float_as_uint(f[4 * v + 1]),
+                                           __float_as_uint(f[4 * v + 2]), __float_as_uint(f[4 * v + 3])));
         } else if constexpr (VEC == 2) {
             *reinterpret_cast<float2*>(q) = make_float2(f[0], f[1]);
         } else {
