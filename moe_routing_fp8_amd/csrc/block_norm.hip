@@ -77,24 +77,27 @@ struct NormArgs {
     float* pre_rstd;
 };
 
-// Thread i's j-th vector of a row starts at element (i + j * blockDim.x) * VEC.
-// VEC == 8 needs 16-byte aligned rows and H % 8 == 0; VEC == 1 takes any.
-template <typename TR, typename TA, int VEC, int VPT, bool STREAM>
+// Parameters are read where the next row finds them again: never streaming.
+template <Access AS>
+using Param8 = Vec8<F32, AS == kOdd ? kOdd : kAligned>;
+
+// Thread i's j-th vector of a row starts at element (i + j * blockDim.x) * 8.
+template <typename TR, typename TA, int VPT, Access AS>
 __global__ __launch_bounds__(kMaxRowThreads) void block_norm_kernel(NormArgs a) {
     __shared__ float part[2][kMaxRowThreads / kWave];
     const int64_t t = blockIdx.x;
     const int H = a.hidden;
     const float inv_h = 1.0f / static_cast<float>(H);
-    float r[VPT][VEC], u[VPT][VEC];
+    float r[VPT][8], u[VPT][8];
     float sq = 0.0f;
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
-        const int e = (threadIdx.x + j * blockDim.x) * VEC;
+        const int e = (threadIdx.x + j * blockDim.x) * 8;
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) r[j][i] = u[j][i] = 0.0f;
+        for (int i = 0; i < 8; ++i) r[j][i] = u[j][i] = 0.0f;
         if (e < H) {
-            TR::template load<VEC, STREAM>(a.residual, t * a.residual_stride + e, r[j]);
-            if (a.y != nullptr) TA::template load<VEC, STREAM>(a.y, t * a.y_stride + e, u[j]);
+            Vec8<TR, AS>::load(a.residual, t * a.residual_stride + e, H - e, r[j]);
+            if (a.y != nullptr) Vec8<TA, AS>::load(a.y, t * a.y_stride + e, H - e, u[j]);
         }
     }
     if (a.y != nullptr) {
@@ -103,26 +106,26 @@ __global__ __launch_bounds__(kMaxRowThreads) void block_norm_kernel(NormArgs a) 
 #pragma unroll
             for (int j = 0; j < VPT; ++j)
 #pragma unroll
-                for (int i = 0; i < VEC; ++i) sq += u[j][i] * u[j][i];
+                for (int i = 0; i < 8; ++i) sq += u[j][i] * u[j][i];
             rstd = rsqrt_f32(block_sum(sq, part[0]) * inv_h + a.eps);
             if (threadIdx.x == 0 && a.post_rstd != nullptr) a.post_rstd[t] = rstd;
         }
         const float token_gate = a.gate_mode == MOE_GATE_TOKEN ? a.gate[t] : 1.0f;
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
-            const int e = (threadIdx.x + j * blockDim.x) * VEC;
+            const int e = (threadIdx.x + j * blockDim.x) * 8;
             if (e >= H) continue;
-            float w[VEC], g[VEC];
+            float w[8], g[8];
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) {
+            for (int i = 0; i < 8; ++i) {
                 w[i] = 1.0f;
                 g[i] = token_gate;
             }
-            if (a.post_weight != nullptr) F32::load<VEC>(a.post_weight, e, w);
-            if (a.gate_mode == MOE_GATE_CHANNEL) F32::load<VEC>(a.gate, e, g);
+            if (a.post_weight != nullptr) Param8<AS>::load(a.post_weight, e, H - e, w);
+            if (a.gate_mode == MOE_GATE_CHANNEL) Param8<AS>::load(a.gate, e, H - e, g);
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) r[j][i] = a.residual_scale * r[j][i] + g[i] * (u[j][i] * rstd * w[i]);
-            TR::template store<VEC, STREAM>(a.res_out, t * H + e, r[j]);
+            for (int i = 0; i < 8; ++i) r[j][i] = a.residual_scale * r[j][i] + g[i] * (u[j][i] * rstd * w[i]);
+            Vec8<TR, AS>::store(a.res_out, t * H + e, H - e, r[j]);
         }
     }
     if (a.normed == nullptr) return;
@@ -130,18 +133,18 @@ __global__ __launch_bounds__(kMaxRowThreads) void block_norm_kernel(NormArgs a) 
 #pragma unroll
     for (int j = 0; j < VPT; ++j)
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) sq += r[j][i] * r[j][i];
+        for (int i = 0; i < 8; ++i) sq += r[j][i] * r[j][i];
     const float rstd = rsqrt_f32(block_sum(sq, part[1]) * inv_h + a.eps);
     if (threadIdx.x == 0 && a.pre_rstd != nullptr) a.pre_rstd[t] = rstd;
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
-        const int e = (threadIdx.x + j * blockDim.x) * VEC;
+        const int e = (threadIdx.x + j * blockDim.x) * 8;
         if (e >= H) continue;
-        float w[VEC];
-        F32::load<VEC>(a.pre_weight, e, w);
+        float w[8];
+        Param8<AS>::load(a.pre_weight, e, H - e, w);
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) w[i] = r[j][i] * rstd * w[i];
-        TA::template store<VEC, STREAM>(a.normed, t * H + e, w);
+        for (int i = 0; i < 8; ++i) w[i] = r[j][i] * rstd * w[i];
+        Vec8<TA, AS>::store(a.normed, t * H + e, H - e, w);
     }
 }
 
@@ -164,15 +167,15 @@ struct NormGradArgs {
     void* grad_residual;
     void* grad_y;
     float* grad_token_gate;
-    float* partials;  // [workgroup][parameter][H], parameters: post weight, channel gate, pre weight (those given)
+    float* partials;  // [workgroup][parameter][H rounded up to 8]: post weight, channel gate, pre weight (those given)
     int num_params;
 };
 
 // A row's four arrays as loaded.
-template <typename TR, typename TA, int VEC, int VPT>
+template <typename TR, typename TA, int VPT, Access AS>
 struct GradRow {
-    typename TR::template Raw<VEC> grad_res_out[VPT], res_out[VPT];
-    typename TA::template Raw<VEC> grad_normed[VPT], y[VPT];
+    Vec8<TR, AS> grad_res_out[VPT], res_out[VPT];
+    Vec8<TA, AS> grad_normed[VPT], y[VPT];
     float pre_rstd, post_rstd, token_gate;
 };
 
@@ -181,9 +184,10 @@ struct GradRow {
 // hidden 7168, so nothing else would cover a row's loads; reading the three
 // parameters again for each row would add 86 KB from the caches to the 129 KB
 // of the row.  Without (rows of more than 8 values a thread): neither fits.
-template <typename TR, typename TA, int VEC, int VPT, bool STREAM>
+// AS: of the loads; OUT: of the stores.
+template <typename TR, typename TA, int VPT, Access AS, Access OUT>
 __global__ __launch_bounds__(kMaxRowThreads) void block_norm_grad_kernel(NormGradArgs a) {
-    constexpr bool HELD = VEC * VPT <= 8;
+    constexpr bool HELD = VPT == 1;
     // two sets in turn: a row's sums have been read before the next row but one writes there
     __shared__ float part[2][3][kMaxRowThreads / kWave];
     int turn = 0;
@@ -191,29 +195,29 @@ __global__ __launch_bounds__(kMaxRowThreads) void block_norm_grad_kernel(NormGra
     const float inv_h = 1.0f / static_cast<float>(H);
     const bool pre = a.grad_normed != nullptr, block = a.y != nullptr, post = a.post_weight != nullptr;
     const bool channel = a.gate_mode == MOE_GATE_CHANNEL;
-    float sum_post[VPT][VEC], sum_gate[VPT][VEC], sum_pre[VPT][VEC];
-    float held_post[HELD ? VPT : 1][VEC], held_gate[HELD ? VPT : 1][VEC], held_pre[HELD ? VPT : 1][VEC];
-    auto load_params = [&](int e, float(&wp)[VEC], float(&wg)[VEC], float(&wn)[VEC]) {
+    float sum_post[VPT][8], sum_gate[VPT][8], sum_pre[VPT][8];
+    float held_post[HELD ? VPT : 1][8], held_gate[HELD ? VPT : 1][8], held_pre[HELD ? VPT : 1][8];
+    auto load_params = [&](int e, float(&wp)[8], float(&wg)[8], float(&wn)[8]) {
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) {
+        for (int i = 0; i < 8; ++i) {
             wp[i] = wg[i] = 1.0f;
             wn[i] = 0.0f;
         }
-        if (post) F32::load<VEC>(a.post_weight, e, wp);
-        if (channel) F32::load<VEC>(a.gate, e, wg);
-        if (pre) F32::load<VEC>(a.pre_weight, e, wn);
+        if (post) Param8<AS>::load(a.post_weight, e, H - e, wp);
+        if (channel) Param8<AS>::load(a.gate, e, H - e, wg);
+        if (pre) Param8<AS>::load(a.pre_weight, e, H - e, wn);
     };
-    auto load = [&](GradRow<TR, TA, VEC, VPT>& row, int64_t t) {
+    auto load = [&](GradRow<TR, TA, VPT, AS>& row, int64_t t) {
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
-            const int e = (threadIdx.x + j * blockDim.x) * VEC;
+            const int e = (threadIdx.x + j * blockDim.x) * 8;
             if (e >= H) continue;
-            if (a.grad_res_out != nullptr) row.grad_res_out[j].load(a.grad_res_out, t * H + e);
+            if (a.grad_res_out != nullptr) row.grad_res_out[j].load(a.grad_res_out, t * H + e, H - e);
             if (pre) {
-                row.res_out[j].load(a.res_out, t * a.res_out_stride + e);
-                row.grad_normed[j].load(a.grad_normed, t * H + e);
+                row.res_out[j].load(a.res_out, t * a.res_out_stride + e, H - e);
+                row.grad_normed[j].load(a.grad_normed, t * H + e, H - e);
             }
-            if (block) row.y[j].load(a.y, t * a.y_stride + e);
+            if (block) row.y[j].load(a.y, t * a.y_stride + e, H - e);
         }
         row.pre_rstd = pre ? a.pre_rstd[t] : 0.0f;
         row.post_rstd = post ? a.post_rstd[t] : 1.0f;
@@ -222,34 +226,34 @@ __global__ __launch_bounds__(kMaxRowThreads) void block_norm_grad_kernel(NormGra
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) sum_post[j][i] = sum_gate[j][i] = sum_pre[j][i] = 0.0f;
-        const int e = (threadIdx.x + j * blockDim.x) * VEC;
+        for (int i = 0; i < 8; ++i) sum_post[j][i] = sum_gate[j][i] = sum_pre[j][i] = 0.0f;
+        const int e = (threadIdx.x + j * blockDim.x) * 8;
         if constexpr (HELD)
             if (e < H) load_params(e, held_post[j], held_gate[j], held_pre[j]);
     }
-    GradRow<TR, TA, VEC, VPT> row;
+    GradRow<TR, TA, VPT, AS> row;
     if constexpr (HELD) load(row, blockIdx.x);
     for (int64_t t = blockIdx.x; t < a.num_tokens; t += gridDim.x, turn ^= 1) {
         if constexpr (!HELD) load(row, t);
-        float d[VPT][VEC], yh[VPT][VEC], xh[VPT][VEC], g[VPT][VEC];
+        float d[VPT][8], yh[VPT][8], xh[VPT][8], g[VPT][8];
         const float pre_rstd = row.pre_rstd, post_rstd = row.post_rstd, token_gate = row.token_gate;
         float dot = 0.0f;
         // D = dr' + rstd * (g - xh * mean(g * xh)), g = dn * pre_weight
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
-            const int e = (threadIdx.x + j * blockDim.x) * VEC;
+            const int e = (threadIdx.x + j * blockDim.x) * 8;
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) d[j][i] = yh[j][i] = xh[j][i] = g[j][i] = 0.0f;
+            for (int i = 0; i < 8; ++i) d[j][i] = yh[j][i] = xh[j][i] = g[j][i] = 0.0f;
             if (e >= H) continue;
             if (a.grad_res_out != nullptr) row.grad_res_out[j].unpack(d[j]);
             if (block) row.y[j].unpack(yh[j]);
             if (pre) {
                 row.res_out[j].unpack(xh[j]);
                 row.grad_normed[j].unpack(g[j]);
-                float wn[VEC];
-                if constexpr (!HELD) F32::load<VEC>(a.pre_weight, e, wn);
+                float wn[8];
+                if constexpr (!HELD) Param8<AS>::load(a.pre_weight, e, H - e, wn);
 #pragma unroll
-                for (int i = 0; i < VEC; ++i) {
+                for (int i = 0; i < 8; ++i) {
                     xh[j][i] *= pre_rstd;
                     sum_pre[j][i] = __builtin_fmaf(g[j][i], xh[j][i], sum_pre[j][i]);
                     g[j][i] *= HELD ? held_pre[HELD ? j : 0][i] : wn[i];
@@ -264,28 +268,28 @@ __global__ __launch_bounds__(kMaxRowThreads) void block_norm_grad_kernel(NormGra
 #pragma unroll
             for (int j = 0; j < VPT; ++j)
 #pragma unroll
-                for (int i = 0; i < VEC; ++i) d[j][i] += pre_rstd * (g[j][i] - xh[j][i] * mean);
+                for (int i = 0; i < 8; ++i) d[j][i] += pre_rstd * (g[j][i] - xh[j][i] * mean);
         }
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
-            const int e = (threadIdx.x + j * blockDim.x) * VEC;
+            const int e = (threadIdx.x + j * blockDim.x) * 8;
             if (e >= H) continue;
-            float o[VEC];
+            float o[8];
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) o[i] = a.residual_scale * d[j][i];
-            TR::template store<VEC, STREAM>(a.grad_residual, t * H + e, o);
+            for (int i = 0; i < 8; ++i) o[i] = a.residual_scale * d[j][i];
+            Vec8<TR, OUT>::store(a.grad_residual, t * H + e, H - e, o);
         }
         if (block) {
             float dot_gate = 0.0f;
             dot = 0.0f;
 #pragma unroll
             for (int j = 0; j < VPT; ++j) {
-                const int e = (threadIdx.x + j * blockDim.x) * VEC;
+                const int e = (threadIdx.x + j * blockDim.x) * 8;
                 if (e >= H) continue;
-                float wp[VEC], wg[VEC], wn[VEC];
+                float wp[8], wg[8], wn[8];
                 if constexpr (!HELD) load_params(e, wp, wg, wn);
 #pragma unroll
-                for (int i = 0; i < VEC; ++i) {
+                for (int i = 0; i < 8; ++i) {
                     const float w = HELD ? held_post[HELD ? j : 0][i] : wp[i];
                     const float gate = channel ? (HELD ? held_gate[HELD ? j : 0][i] : wg[i]) : token_gate;
                     yh[j][i] *= post_rstd;
@@ -307,30 +311,32 @@ __global__ __launch_bounds__(kMaxRowThreads) void block_norm_grad_kernel(NormGra
 #pragma unroll
                 for (int j = 0; j < VPT; ++j)
 #pragma unroll
-                    for (int i = 0; i < VEC; ++i) d[j][i] = post_rstd * (d[j][i] - yh[j][i] * mean);
+                    for (int i = 0; i < 8; ++i) d[j][i] = post_rstd * (d[j][i] - yh[j][i] * mean);
             }
 #pragma unroll
             for (int j = 0; j < VPT; ++j) {
-                const int e = (threadIdx.x + j * blockDim.x) * VEC;
-                if (e < H) TA::template store<VEC, STREAM>(a.grad_y, t * H + e, d[j]);
+                const int e = (threadIdx.x + j * blockDim.x) * 8;
+                if (e < H) Vec8<TA, OUT>::store(a.grad_y, t * H + e, H - e, d[j]);
             }
         }
     }
-    float* out = a.partials + static_cast<int64_t>(blockIdx.x) * a.num_params * H;
+    const int width = (H + 7) / 8 * 8;
+    float* out = a.partials + static_cast<int64_t>(blockIdx.x) * a.num_params * width;
+    using Out8 = Vec8<F32, kAligned>;
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
-        const int e = (threadIdx.x + j * blockDim.x) * VEC;
+        const int e = (threadIdx.x + j * blockDim.x) * 8;
         if (e >= H) continue;
         int64_t at = e;
         if (post) {
-            F32::store<VEC>(out, at, sum_post[j]);
-            at += H;
+            Out8::store(out, at, 8, sum_post[j]);
+            at += width;
         }
         if (channel) {
-            F32::store<VEC>(out, at, sum_gate[j]);
-            at += H;
+            Out8::store(out, at, 8, sum_gate[j]);
+            at += width;
         }
-        if (pre) F32::store<VEC>(out, at, sum_pre[j]);
+        if (pre) Out8::store(out, at, 8, sum_pre[j]);
     }
 }
 
@@ -338,11 +344,11 @@ __global__ __launch_bounds__(kMaxRowThreads) void block_norm_grad_kernel(NormGra
 // kSumWaves waves every kSumWaves-th row in order, then the waves in order.
 constexpr int kSumWaves = 16;
 __global__ __launch_bounds__(kSumWaves* kWave) void block_norm_param_kernel(const float* __restrict__ partials,
-                                                                             int64_t blocks, int width, int H,
+                                                                             int64_t blocks, int params, int H,
                                                                              float* o0, float* o1, float* o2) {
     __shared__ float lds[kSumWaves][kWave];
     const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
-    const int c = blockIdx.x * kWave + lane;
+    const int c = blockIdx.x * kWave + lane, padded = (H + 7) / 8 * 8, width = params * padded;
     float v = 0.0f;
     if (c < width)
 #pragma unroll 8
@@ -357,55 +363,47 @@ __global__ __launch_bounds__(kSumWaves* kWave) void block_norm_param_kernel(cons
         int left = c;
         for (int k = 0; k < 3; ++k) {
             if (outs[k] == nullptr) continue;
-            if (left < H) {
-                outs[k][left] = s;
+            if (left < padded) {
+                if (left < H) outs[k][left] = s;
                 break;
             }
-            left -= H;
+            left -= padded;
         }
     }
 }
 
-// Threads of a row: enough that VPT vectors of VEC each cover it, in whole waves.
-int row_threads(int H, int vec, int vpt) {
-    const int n = (H + vec * vpt - 1) / (vec * vpt);
+// Threads of a row: enough that VPT vectors of 8 each cover it, in whole waves.
+int row_threads(int H, int vpt) {
+    const int n = (H + 8 * vpt - 1) / (8 * vpt);
     return (n + kWave - 1) / kWave * kWave;
 }
 
-template <typename TR, typename TA, int VEC, int VPT, bool STREAM>
+template <typename TR, typename TA, int VPT, Access AS>
 hipError_t launch_norm(const NormArgs& a, hipStream_t stream) {
-    hipLaunchKernelGGL((block_norm_kernel<TR, TA, VEC, VPT, STREAM>), dim3(static_cast<unsigned>(a.num_tokens)),
-                       dim3(row_threads(a.hidden, VEC, VPT)), 0, stream, a);
+    hipLaunchKernelGGL((block_norm_kernel<TR, TA, VPT, AS>), dim3(static_cast<unsigned>(a.num_tokens)),
+                       dim3(row_threads(a.hidden, VPT)), 0, stream, a);
     return hipGetLastError();
 }
 // Two vectors a thread where the rows fill the chip (their shorter workgroups
 // overlap: 48.0 us against 50.8 with one) or do not fit otherwise; one where
 // the latency of a few rows counts.
-template <typename TR, typename TA>
-hipError_t launch_norm_types(const NormArgs& a, bool vec, bool far, hipStream_t stream) {
-    if (!vec)
-        return a.hidden <= 4 * kMaxRowThreads ? launch_norm<TR, TA, 1, 4, false>(a, stream)
-                                              : launch_norm<TR, TA, 1, 16, false>(a, stream);
-    if (far) return launch_norm<TR, TA, 8, 2, true>(a, stream);
-    if (a.hidden <= 8 * kMaxRowThreads && a.num_tokens <= 2 * kComputeUnits)
-        return launch_norm<TR, TA, 8, 1, false>(a, stream);
-    return launch_norm<TR, TA, 8, 2, false>(a, stream);
+template <typename TR, typename TA, Access AS>
+hipError_t launch_norm_rows(const NormArgs& a, hipStream_t stream) {
+    if (AS != kStreaming && a.hidden <= 8 * kMaxRowThreads && a.num_tokens <= 2 * kComputeUnits)
+        return launch_norm<TR, TA, 1, AS>(a, stream);
+    return launch_norm<TR, TA, 2, AS>(a, stream);
 }
 
-template <typename TR, typename TA, int VEC, int VPT, bool STREAM>
+template <typename TR, typename TA, int VPT, Access AS, Access OUT>
 hipError_t launch_grad(const NormGradArgs& a, int64_t blocks, hipStream_t stream) {
-    hipLaunchKernelGGL((block_norm_grad_kernel<TR, TA, VEC, VPT, STREAM>), dim3(static_cast<unsigned>(blocks)),
-                       dim3(row_threads(a.hidden, VEC, VPT)), 0, stream, a);
+    hipLaunchKernelGGL((block_norm_grad_kernel<TR, TA, VPT, AS, OUT>), dim3(static_cast<unsigned>(blocks)),
+                       dim3(row_threads(a.hidden, VPT)), 0, stream, a);
     return hipGetLastError();
 }
-template <typename TR, typename TA>
-hipError_t launch_grad_types(const NormGradArgs& a, int64_t blocks, bool vec, bool far, hipStream_t stream) {
-    if (!vec)
-        return a.hidden <= 4 * kMaxRowThreads ? launch_grad<TR, TA, 1, 4, false>(a, blocks, stream)
-                                              : launch_grad<TR, TA, 1, 16, false>(a, blocks, stream);
-    if (a.hidden > 8 * kMaxRowThreads) return launch_grad<TR, TA, 8, 2, false>(a, blocks, stream);
-    return far ? launch_grad<TR, TA, 8, 1, true>(a, blocks, stream)
-               : launch_grad<TR, TA, 8, 1, false>(a, blocks, stream);
+template <typename TR, typename TA, Access AS, Access OUT>
+hipError_t launch_grad_rows(const NormGradArgs& a, int64_t blocks, hipStream_t stream) {
+    if (a.hidden > 8 * kMaxRowThreads) return launch_grad<TR, TA, 2, AS, AS>(a, blocks, stream);
+    return launch_grad<TR, TA, 1, AS, OUT>(a, blocks, stream);
 }
 
 // Calls f with the two element types.
@@ -423,7 +421,7 @@ bool vec_rows(const void* p, int64_t stride, int32_t dtype) {
 }
 
 int64_t grad_blocks(int64_t T, int H) {
-    const int waves = row_threads(H, 8, 1) / kWave;
+    const int waves = row_threads(H, 1) / kWave;
     const int64_t most = kComputeUnits * (waves > 8 ? 1 : waves > 4 ? 2 : 4);
     return T < most ? T : most;
 }
@@ -472,13 +470,17 @@ moe_status moe_block_norm(const void* residual, int64_t residual_stride, int32_t
     const int64_t row_bytes = int64_t{2} * hidden * (rb + ab);
     const bool far = num_tokens * row_bytes > kStreamBytes;
     return hip_status(with_types(residual_dtype, act_dtype, [&](auto r, auto x) {
-        return launch_norm_types<decltype(r), decltype(x)>(a, vec, far, stream);
+        using R = decltype(r);
+        using A = decltype(x);
+        return !vec  ? launch_norm_rows<R, A, kOdd>(a, stream)
+               : far ? launch_norm_rows<R, A, kStreaming>(a, stream)
+                     : launch_norm_rows<R, A, kAligned>(a, stream);
     }));
 }
 
 size_t moe_block_norm_backward_workspace_bytes(int64_t num_tokens, int32_t hidden) {
     if (num_tokens < 0 || num_tokens > MOE_BLOCK_NORM_MAX_TOKENS || hidden < 1 || hidden > moe::kMaxHidden) return 0;
-    const size_t n = static_cast<size_t>(moe::grad_blocks(num_tokens, hidden)) * 3 * static_cast<size_t>(hidden) * 4;
+    const size_t n = static_cast<size_t>(moe::grad_blocks(num_tokens, hidden)) * 3 * ((hidden + 7) / 8 * 8) * 4;
     return (n + 255) / 256 * 256;
 }
 
@@ -562,15 +564,19 @@ moe_status moe_block_norm_backward(const void* grad_res_out, const void* grad_no
                              params};
         const bool far = num_tokens * (int64_t{3} * hidden * (rb + ab)) > kStreamBytes;
         const hipError_t err = with_types(residual_dtype, act_dtype, [&](auto r, auto x) {
-            return launch_grad_types<decltype(r), decltype(x)>(a, blocks, vec, far, stream);
+            using R = decltype(r);
+            using A = decltype(x);
+            return !vec  ? launch_grad_rows<R, A, kOdd, kOdd>(a, blocks, stream)
+                   : far ? launch_grad_rows<R, A, kAligned, kStreaming>(a, blocks, stream)
+                         : launch_grad_rows<R, A, kAligned, kAligned>(a, blocks, stream);
         });
         if (err != hipSuccess) return hip_status(err);
     }
     if (params == 0) return MOE_OK;
     // with no tokens the parameters' gradients are zero: the same sums over no workgroups
-    const int width = params * hidden;
+    const int width = params * ((hidden + 7) / 8 * 8);
     hipLaunchKernelGGL(block_norm_param_kernel, dim3((width + kWave - 1) / kWave), dim3(kSumWaves * kWave), 0, stream,
-                       partials, blocks, width, hidden, grad_post_weight, channel ? grad_gate : nullptr,
+                       partials, blocks, params, hidden, grad_post_weight, channel ? grad_gate : nullptr,
                        grad_pre_weight);
     return hip_status(hipGetLastError());
 }

@@ -79,52 +79,18 @@ __device__ __forceinline__ uint32_t bf16_pack2(float lo, float hi) {
     return static_cast<uint32_t>(bf16_bits(lo)) | (static_cast<uint32_t>(bf16_bits(hi)) << 16);
 }
 
-template <bool STREAM>
-__device__ __forceinline__ uint4 load16(const uint4* p) {
-    if constexpr (STREAM) return load_stream16(p);
-    return *p;
-}
-template <bool STREAM>
-__device__ __forceinline__ void store16(uint4* p, const uint4& v) {
-    if constexpr (STREAM)
-        store_stream16(p, v);
-    else
-        *p = v;
-}
-
 // Element types of the operators that take bf16 or fp32: VEC consecutive
 // values to and from fp32 registers.  VEC > 1 needs the address aligned to
-// min(16, VEC * sizeof(T)) bytes.  STREAM: non-temporal 16-byte accesses.
-//
-// Raw<VEC>: the values as loaded, to be unpacked later.
+// min(16, VEC * sizeof(T)) bytes.
 struct Bf16 {
     static constexpr int kBytes = 2;
     template <int VEC>
-    struct Raw {
-        static_assert(VEC == 8 || VEC == 1, "vector width");
-        typename std::conditional<VEC == 8, u32x4_t, uint16_t>::type v;
-        __device__ __forceinline__ void load(const void* p, int64_t i) {
-            v = *reinterpret_cast<const decltype(v)*>(static_cast<const uint16_t*>(p) + i);
-        }
-        __device__ __forceinline__ void unpack(float (&f)[VEC]) const {
-            if constexpr (VEC == 8) {
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    f[2 * k] = bf16_lo(v[k]);
-                    f[2 * k + 1] = bf16_hi(v[k]);
-                }
-            } else {
-                f[0] = __uint_as_float(static_cast<uint32_t>(v) << 16);
-            }
-        }
-    };
-    template <int VEC, bool STREAM = false>
     static __device__ __forceinline__ void load(const void* p, int64_t i, float (&f)[VEC]) {
         const uint16_t* q = static_cast<const uint16_t*>(p) + i;
         if constexpr (VEC % 8 == 0) {
 #pragma unroll
             for (int v = 0; v < VEC / 8; ++v)
-                unpack8_bf16(load16<STREAM>(reinterpret_cast<const uint4*>(q) + v),
+                unpack8_bf16(reinterpret_cast<const uint4*>(q)[v],
                              *reinterpret_cast<float(*)[8]>(f + 8 * v));
         } else if constexpr (VEC == 4) {
             const uint2 r = *reinterpret_cast<const uint2*>(q);
@@ -137,16 +103,15 @@ struct Bf16 {
             f[0] = __uint_as_float(static_cast<uint32_t>(*q) << 16);
         }
     }
-    template <int VEC, bool STREAM = false>
+    template <int VEC>
     static __device__ __forceinline__ void store(void* p, int64_t i, const float (&f)[VEC]) {
         uint16_t* q = static_cast<uint16_t*>(p) + i;
         if constexpr (VEC % 8 == 0) {
 #pragma unroll
             for (int v = 0; v < VEC / 8; ++v) {
                 const float* g = f + 8 * v;
-                store16<STREAM>(reinterpret_cast<uint4*>(q) + v,
-                                make_uint4(bf16_pack2(g[0], g[1]), bf16_pack2(g[2], g[3]), bf16_pack2(g[4], g[5]),
-                                           bf16_pack2(g[6], g[7])));
+                reinterpret_cast<uint4*>(q)[v] = make_uint4(bf16_pack2(g[0], g[1]), bf16_pack2(g[2], g[3]),
+                                                            bf16_pack2(g[4], g[5]), bf16_pack2(g[6], g[7]));
             }
         } else if constexpr (VEC == 4) {
             *reinterpret_cast<uint2*>(q) = make_uint2(bf16_pack2(f[0], f[1]), bf16_pack2(f[2], f[3]));
@@ -162,31 +127,12 @@ struct Bf16 {
 struct F32 {
     static constexpr int kBytes = 4;
     template <int VEC>
-    struct Raw {
-        static_assert(VEC == 8 || VEC == 1, "vector width");
-        static constexpr int N = VEC == 8 ? 2 : 1;
-        typename std::conditional<VEC == 8, u32x4_t, uint32_t>::type v[N];
-        __device__ __forceinline__ void load(const void* p, int64_t i) {
-#pragma unroll
-            for (int n = 0; n < N; ++n)
-                v[n] = reinterpret_cast<const std::remove_reference_t<decltype(v[0])>*>(static_cast<const float*>(p) + i)[n];
-        }
-        __device__ __forceinline__ void unpack(float (&f)[VEC]) const {
-            if constexpr (VEC == 8) {
-#pragma unroll
-                for (int k = 0; k < 8; ++k) f[k] = __uint_as_float(v[k / 4][k % 4]);
-            } else {
-                f[0] = __uint_as_float(v[0]);
-            }
-        }
-    };
-    template <int VEC, bool STREAM = false>
     static __device__ __forceinline__ void load(const void* p, int64_t i, float (&f)[VEC]) {
         const float* q = static_cast<const float*>(p) + i;
         if constexpr (VEC % 4 == 0) {
 #pragma unroll
             for (int v = 0; v < VEC / 4; ++v) {
-                const uint4 r = load16<STREAM>(reinterpret_cast<const uint4*>(q) + v);
+                const uint4 r = reinterpret_cast<const uint4*>(q)[v];
                 f[4 * v] = __uint_as_float(r.x); f[4 * v + 1] = __uint_as_float(r.y);
                 f[4 * v + 2] = __uint_as_float(r.z); f[4 * v + 3] = __uint_as_float(r.w);
             }
@@ -198,21 +144,109 @@ struct F32 {
             f[0] = *q;
         }
     }
-    template <int VEC, bool STREAM = false>
+    template <int VEC>
     static __device__ __forceinline__ void store(void* p, int64_t i, const float (&f)[VEC]) {
         float* q = static_cast<float*>(p) + i;
         if constexpr (VEC % 4 == 0) {
 #pragma unroll
             for (int v = 0; v < VEC / 4; ++v)
-                store16<STREAM>(reinterpret_cast<uint4*>(q) + v,
-                                make_uint4(__float_as_uint(f[4 * v]), __float_as_uint(f[4 * v + 1]),
-                                           __float_as_uint(f[4 * v + 2]), __float_as_uint(f[4 * v + 3])));
+                reinterpret_cast<float4*>(q)[v] = make_float4(f[4 * v], f[4 * v + 1], f[4 * v + 2], f[4 * v + 3]);
         } else if constexpr (VEC == 2) {
             *reinterpret_cast<float2*>(q) = make_float2(f[0], f[1]);
         } else {
             static_assert(VEC == 1, "vector width");
             *q = f[0];
         }
+    }
+};
+
+// Eight consecutive values of a row of T (Bf16 or F32), as loaded.  AS says
+// how: kAligned 16-byte accesses, the same kStreaming past the caches, or
+// kOdd, for rows of any alignment and length: 16-byte accesses at the
+// element's alignment (the hardware splits what crosses a line) and, for the
+// last n < 8 values of a row, one by one.
+enum Access { kAligned, kStreaming, kOdd };
+
+template <typename T, Access AS>
+struct Vec8 {
+    static constexpr int N = T::kBytes / 2;  // 16-byte pieces
+    struct __attribute__((packed, aligned(T::kBytes))) Piece {
+        u32x4_t v;
+    };
+    u32x4_t v[N];
+
+    // n: values left in the row from i on
+    __device__ __forceinline__ void load(const void* p, int64_t i, int n) {
+        const uint8_t* q = static_cast<const uint8_t*>(p) + i * T::kBytes;
+        if constexpr (AS == kOdd) {
+            if (n >= 8) {
+#pragma unroll
+                for (int k = 0; k < N; ++k) v[k] = reinterpret_cast<const Piece*>(q)[k].v;
+            } else {
+                uint32_t w[4 * N] = {};
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    if (k >= n) continue;
+                    if constexpr (T::kBytes == 2)
+                        w[k / 2] |= static_cast<uint32_t>(reinterpret_cast<const uint16_t*>(q)[k]) << (k % 2 * 16);
+                    else
+                        w[k] = reinterpret_cast<const uint32_t*>(q)[k];
+                }
+#pragma unroll
+                for (int k = 0; k < 4 * N; ++k) v[k / 4][k % 4] = w[k];
+            }
+        } else {
+#pragma unroll
+            for (int k = 0; k < N; ++k) {
+                const u32x4_t* a = reinterpret_cast<const u32x4_t*>(q) + k;
+                v[k] = AS == kStreaming ? __builtin_nontemporal_load(a) : *a;
+            }
+        }
+    }
+    __device__ __forceinline__ void unpack(float (&f)[8]) const {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            if constexpr (T::kBytes == 2)
+                f[k] = k % 2 == 0 ? bf16_lo(v[0][k / 2]) : bf16_hi(v[0][k / 2]);
+            else
+                f[k] = __uint_as_float(v[k / 4][k % 4]);
+        }
+    }
+    static __device__ __forceinline__ void store(void* p, int64_t i, int n, const float (&f)[8]) {
+        uint8_t* q = static_cast<uint8_t*>(p) + i * T::kBytes;
+        if (AS == kOdd && n < 8) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                if (k >= n) continue;
+                if constexpr (T::kBytes == 2)
+                    reinterpret_cast<uint16_t*>(q)[k] = bf16_bits(f[k]);
+                else
+                    reinterpret_cast<float*>(q)[k] = f[k];
+            }
+            return;
+        }
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+            u32x4_t w;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                if constexpr (T::kBytes == 2)
+                    w[c] = bf16_pack2(f[2 * c], f[2 * c + 1]);
+                else
+                    w[c] = __float_as_uint(f[4 * k + c]);
+            }
+            if constexpr (AS == kOdd)
+                reinterpret_cast<Piece*>(q)[k].v = w;
+            else if constexpr (AS == kStreaming)
+                __builtin_nontemporal_store(w, reinterpret_cast<u32x4_t*>(q) + k);
+            else
+                reinterpret_cast<u32x4_t*>(q)[k] = w;
+        }
+    }
+    static __device__ __forceinline__ void load(const void* p, int64_t i, int n, float (&f)[8]) {
+        Vec8 r;
+        r.load(p, i, n);
+        r.unpack(f);
     }
 };
 
