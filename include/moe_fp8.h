@@ -429,7 +429,7 @@ moe_status swiglu_cast(const uint16_t* gate_up_bf16, int64_t num_rows, int32_t i
 #define MOE_GATE_TOKEN 2   /* gate fp32 [num_tokens]: one value per token */
 
 #define MOE_BLOCK_NORM_MAX_HIDDEN 16384
-#define MOE_BLOCK_NORM_MAX_TOKENS 4194304
+#define MOE_BLOCK_NORM_MAX_TOKENS 4194303 /* a workgroup of up to 1024 threads each, below 2^32 threads */
 
 /*
  * moe_block_norm -- what stands between two blocks of the residual stream: the

@@ -7,6 +7,7 @@ There is no CPU fallback: without the built library every call raises.
 """
 import contextlib
 import ctypes
+import functools
 import os
 import re
 from typing import Optional, Tuple
@@ -866,6 +867,7 @@ def moe_block_norm(residual: torch.Tensor, y: Optional[torch.Tensor] = None,
     return out
 
 
+@functools.lru_cache(maxsize=256)
 def moe_block_norm_backward_workspace_bytes(num_tokens: int, hidden: int) -> int:
     return int(lib().moe_block_norm_backward_workspace_bytes(num_tokens, hidden))
 
@@ -953,10 +955,12 @@ def _balance_inputs(logits, score, token_mask, seq_offsets):
         seqs = seq_offsets.shape[0] - 1
         if seqs < 1:
             raise ValueError("seq_offsets: expected at least two entries")
-    _device(logits, token_mask, seq_offsets)
+    if token_mask is not None or seq_offsets is not None:
+        _device(logits, token_mask, seq_offsets)
     return stride, _SCORES[score], seqs
 
 
+@functools.lru_cache(maxsize=256)
 def moe_balance_loss_workspace_bytes(num_tokens: int, num_experts: int, num_seqs: int = 1) -> int:
     return int(lib().moe_balance_loss_workspace_bytes(num_tokens, num_experts, num_seqs))
 
@@ -973,7 +977,9 @@ def moe_balance_loss(logits: torch.Tensor, topk_idx: torch.Tensor, score: str = 
     _need(topk_idx, torch.int64, 2, "topk_idx")
     K = topk_idx.shape[1]
     _shape(topk_idx, (T, K), "topk_idx")
-    dev = _device(logits, topk_idx)
+    dev = logits.device
+    if topk_idx.device != dev:
+        _device(logits, topk_idx)
     if out is None:
         with _alloc_on(stream):
             out = {"loss": torch.empty(S, device=dev), "counts": torch.empty((S, E), dtype=torch.int32, device=dev),
@@ -1058,8 +1064,6 @@ def moe_expert_matvec(x: torch.Tensor, w_codes: torch.Tensor, w_sf: torch.Tensor
             out = torch.empty((R, N), dtype=torch.bfloat16, device=dev)
     else:
         _need_out(out, torch.bfloat16, (R, N), "out", dev)
-    if debug_enabled() and not e4m3:
-        _debug_raise("moe_expert_matvec", lambda: moe_check_activations(x, stream=stream), stream)
     _call("moe_expert_matvec", dev, stream, _ptr(x), MOE_DTYPE_E4M3 if e4m3 else MOE_DTYPE_BF16, _ptr(x_sf), X,
           _ptr(row_token), R, K, N, E, _ptr(expert_offsets), _ptr(w_codes), _ptr(w_sf), K // G, int(ue8m0), _ptr(out))
     return out

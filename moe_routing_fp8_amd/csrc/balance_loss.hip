@@ -10,7 +10,7 @@
 //   g_s      = grad_loss[s] * E / (K n_s^2)
 // (the counts are whole numbers and carry no gradient).
 //
-// Forward, two or three launches.  The tokens are cut into chunks of consecutive
+// Forward, one to three launches.  The tokens are cut into chunks of consecutive
 // tokens, one workgroup each; 16 lanes (64 above 256 experts) hold a token's
 // whole row of logits in registers and keep their running sums of p there
 // too.  A chunk may meet
@@ -20,7 +20,8 @@
 // grows, so no two pieces share a slot, and a sequence's slots are
 // consecutive).  Then each sequence's slots are added in a fixed order: by one
 // workgroup per sequence in a second launch where it has few, else by
-// workgroups that take a few columns each, with the loss in a third launch.
+// workgroups that take a few columns each, with the loss in a third launch.  A
+// batch of one chunk takes its losses in the first launch.
 // No floating atomics: the results do not depend on timing.
 // Backward, one launch: the same lanes per token read the row again, with the
 // sequence's counts in registers.
@@ -57,12 +58,17 @@ int rows_per_wave(int E) { return E > kNarrowExperts ? RowShape<64, 16>::kRows :
 constexpr int64_t kFewSeqsChunks = 256;
 constexpr int64_t kManySeqsChunks = 1024;
 constexpr int kManySeqs = 4;
+// Batches of one chunk take one launch: up to this many steps of a workgroup of kMaxWaves waves (256 tokens up to
+// 256 experts), which take less than a second launch, and this many sequences, whose losses are taken in turn.
+constexpr int64_t kOneLaunchSteps = 4;
+constexpr int kOneLaunchSeqs = 8;
 // Up to this many slots per sequence, on average, one workgroup adds all of a sequence's; above, its columns are
 // split over workgroups and the loss takes a launch of its own.
 constexpr int64_t kOneLevelSlots = 64;
 constexpr int kReduceCols = 16;  // columns of a workgroup of the split sum: 64-byte pieces of each slot
 
 struct BalancePlan {
+    bool one_launch;     // one chunk, whose workgroup also takes the losses
     int waves;           // of a workgroup
     int64_t chunk;       // tokens per workgroup: a multiple of waves * rows_per_wave
     int64_t num_chunks;
@@ -78,10 +84,13 @@ BalancePlan plan_balance(int64_t T, int E, int S) {
     BalancePlan p;
     const int64_t most = S >= kManySeqs ? kManySeqsChunks : kFewSeqsChunks;
     const int64_t rows = rows_per_wave(E);
-    p.waves = 4;
-    while (p.waves < kMaxWaves && T > p.waves * rows * most) p.waves *= 2;
+    p.one_launch = T > 0 && T <= kOneLaunchSteps * kMaxWaves * rows && S <= kOneLaunchSeqs;
+    p.waves = p.one_launch ? kMaxWaves : 4;
+    while (p.one_launch && p.waves > 4 && T <= p.waves / 2 * rows) p.waves /= 2;
+    while (!p.one_launch && p.waves < kMaxWaves && T > p.waves * rows * most) p.waves *= 2;
     const int64_t step = p.waves * rows;
-    const int64_t steps = (T + step * most - 1) / (step * most);
+    const int64_t chunks = p.one_launch ? 1 : most;
+    const int64_t steps = (T + step * chunks - 1) / (step * chunks);
     p.chunk = step * (steps > 1 ? steps : 1);
     p.num_chunks = (T + p.chunk - 1) / p.chunk;
     p.num_slots = p.num_chunks + S;
@@ -212,22 +221,49 @@ __device__ __forceinline__ float row_scores(const float (&z)[S::P], float (&w)[S
     return nothing ? 0.0f : 1.0f / sum;
 }
 
+// loss = E / (K n) * sum over e of count * mean, from that sum.
+__device__ __forceinline__ float loss_value(float dot, int E, int K, float many) {
+    return dot * (static_cast<float>(E) / static_cast<float>(K)) / many;
+}
+
+// The outputs, for a batch of one chunk (else all nullptr).
+struct Outputs {
+    float* loss;
+    int32_t* counts;
+    int32_t* seq_tokens;
+    float* prob_mean;
+};
+
 template <typename TL, typename S, int V, bool SIGMOID>
 __global__ __launch_bounds__(kMaxWaves* kWave) void balance_sums_kernel(
     const void* __restrict__ logits, int64_t stride, int E, const int64_t* __restrict__ topk_idx, int K,
     const uint8_t* __restrict__ mask, Seqs seqs, int64_t chunk, float* __restrict__ sums,
-    int32_t* __restrict__ counts, int32_t* __restrict__ tokens) {
+    int32_t* __restrict__ counts, int32_t* __restrict__ tokens, Outputs out) {
     constexpr int P = S::P;
-    extern __shared__ float lds[];  // waves x E sums, then E counts, then one token count
+    extern __shared__ float lds[];  // waves x E sums, then E counts, one token count and a sum of each wave
     const int waves = blockDim.x / kWave;
     int32_t* hist = reinterpret_cast<int32_t*>(lds + waves * E);
     int32_t* live = hist + E;
+    float* wave_dot = reinterpret_cast<float*>(live + 1);
     const int lane = threadIdx.x & (kWave - 1), l = lane % S::L, row = lane / S::L;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int64_t t0 = blockIdx.x * chunk;
     const int64_t t1 = min(t0 + chunk, seqs.num_tokens);
     for (int e = threadIdx.x; e < E; e += blockDim.x) hist[e] = 0;
     if (threadIdx.x == 0) *live = 0;
+    if (out.loss != nullptr) {  // sequences without tokens; the others are written once, below
+        for (int i = 0; i < seqs.num_seqs; ++i) {
+            if (seqs.edge(i) < seqs.edge(i + 1)) continue;
+            for (int e = threadIdx.x; e < E; e += blockDim.x) {
+                out.counts[i * E + e] = 0;
+                if (out.prob_mean != nullptr) out.prob_mean[i * E + e] = 0.0f;
+            }
+            if (threadIdx.x == 0) {
+                out.loss[i] = 0.0f;
+                out.seq_tokens[i] = 0;
+            }
+        }
+    }
 
     float acc[P];
 #pragma unroll
@@ -248,17 +284,39 @@ __global__ __launch_bounds__(kMaxWaves* kWave) void balance_sums_kernel(
         n = 0;
         __syncthreads();
         const int64_t slot = blockIdx.x + static_cast<int64_t>(s);
+        const int all = *live;
+        const float many = all > 0 ? static_cast<float>(all) : 1.0f;
+        float dot = 0.0f;
         for (int e = threadIdx.x; e < E; e += blockDim.x) {
             float v = 0.0f;
 #pragma unroll 4
             for (int w = 0; w < waves; ++w) v += lds[w * E + e];
-            sums[slot * E + e] = v;
-            counts[slot * E + e] = hist[e];
+            if (out.loss != nullptr) {
+                v /= many;
+                out.counts[s * E + e] = hist[e];
+                if (out.prob_mean != nullptr) out.prob_mean[s * E + e] = v;
+                dot += static_cast<float>(hist[e]) * v;
+            } else {
+                sums[slot * E + e] = v;
+                counts[slot * E + e] = hist[e];
+            }
             hist[e] = 0;
         }
+        if (out.loss != nullptr) {
+            dot = wave_sum_f32(dot);
+            if (lane == 0) wave_dot[wave] = dot;
+        }
+        __syncthreads();
         if (threadIdx.x == 0) {
-            tokens[slot] = *live;
             *live = 0;
+            if (out.loss != nullptr) {
+                dot = 0.0f;
+                for (int w = 0; w < waves; ++w) dot += wave_dot[w];
+                out.loss[s] = loss_value(dot, E, K, many);
+                out.seq_tokens[s] = all;
+            } else {
+                tokens[slot] = all;
+            }
         }
         __syncthreads();
     };
@@ -324,11 +382,6 @@ __device__ __forceinline__ int live_tokens(const int32_t* tokens, int64_t first,
     int n = 0;
     for (int64_t i = first + lane; i <= last; i += kWave) n += tokens[i];
     return n;
-}
-
-// loss = E / (K n) * sum over e of count * mean, from the calling wave's lanes' parts of the sum.
-__device__ __forceinline__ float loss_value(float dot, int E, int K, float many) {
-    return dot * (static_cast<float>(E) / static_cast<float>(K)) / many;
 }
 
 // One workgroup per sequence: `cols` threads (a power of two >= E) for each
@@ -553,13 +606,14 @@ struct SumsLauncher {
     BalancePlan plan;
     float* sums;
     int32_t *counts, *tokens;
+    Outputs out;
     hipStream_t stream;
     template <typename TL, typename S, int V, bool SIGMOID>
     hipError_t operator()() const {
-        const size_t lds = (static_cast<size_t>(plan.waves + 1) * E + 1) * sizeof(float);
+        const size_t lds = (static_cast<size_t>(plan.waves + 1) * E + 1 + plan.waves) * sizeof(float);
         hipLaunchKernelGGL((balance_sums_kernel<TL, S, V, SIGMOID>), dim3(static_cast<unsigned>(plan.num_chunks)),
                            dim3(plan.waves * kWave), lds, stream, logits, stride, E, topk_idx, K, mask, seqs, plan.chunk,
-                           sums, counts, tokens);
+                           sums, counts, tokens, out);
         return hipGetLastError();
     }
 };
@@ -634,12 +688,13 @@ moe_status moe_balance_loss(const void* logits, int32_t logits_dtype, int64_t ro
     int32_t* slot_tokens = reinterpret_cast<int32_t*>(ws + plan.sums_bytes + plan.counts_bytes);
     const Seqs seqs{seq_offsets, num_tokens, num_seqs};
     if (num_tokens > 0) {
+        const Outputs out = plan.one_launch ? Outputs{loss, counts, seq_tokens, prob_mean} : Outputs{};
         const SumsLauncher go{logits, row_stride, num_experts, topk_idx, num_topk, token_mask, seqs,
-                              plan,   sums,       slot_counts, slot_tokens, stream};
+                              plan,   sums,       slot_counts, slot_tokens, out, stream};
         const hipError_t err = logits_dtype == MOE_DTYPE_BF16
                                    ? with_row<Bf16>(logits, nullptr, nullptr, row_stride, num_experts, score, go)
                                    : with_row<F32>(logits, nullptr, nullptr, row_stride, num_experts, score, go);
-        if (err != hipSuccess) return hip_status(err);
+        if (err != hipSuccess || plan.one_launch) return hip_status(err);
     }
     const int64_t slots = plan.num_slots / num_seqs;  // of a sequence, on average
     if (slots <= kOneLevelSlots) {

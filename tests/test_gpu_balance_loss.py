@@ -351,3 +351,23 @@ def test_in_a_graph():
         want, gw = _run(d, "sigmoid")
         torch.cuda.synchronize()
         assert all(torch.equal(out[key], want[key]) for key in want) and torch.equal(grad, gw)
+
+
+def test_more_than_2_to_31_elements():
+    """2100000 x 1024 logits in two sequences: the last 50 tokens' gradient and counts are those of these alone."""
+    T, E = 2100000, 1024
+    _log("2.2e9 logits")
+    g = torch.Generator(device="cuda").manual_seed(13)
+    z = torch.empty(T, E, dtype=BF16, device="cuda").normal_(generator=g)
+    ids = torch.randint(0, E, (T, 2), generator=g, device="cuda")
+    off = torch.tensor([0, T - 50, T], dtype=torch.int32, device="cuda")
+    one = torch.ones(2, device="cuda")
+    o = moe.moe_balance_loss(z, ids, seq_offsets=off)
+    grad = moe.moe_balance_loss_backward(one, z, o["counts"], o["seq_tokens"], 2, seq_offsets=off)
+    few = moe.moe_balance_loss(z[-50:].clone(), ids[-50:].clone())
+    alone = moe.moe_balance_loss_backward(one[:1], z[-50:].clone(), few["counts"], few["seq_tokens"], 2)
+    assert o["seq_tokens"].tolist() == [T - 50, 50]
+    assert torch.equal(o["counts"][1], few["counts"][0])
+    assert torch.equal(o["counts"][0], torch.bincount(ids[:-50].flatten(), minlength=E).int())
+    assert abs(float(o["loss"][1] - few["loss"][0])) <= 1e-5 * float(few["loss"][0])  # other order of 50 additions
+    assert torch.equal(grad[-50:], alone)

@@ -401,3 +401,17 @@ def test_in_a_graph():
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(out, want))
         assert all(torch.equal(o[key], wo[key]) for key in wo)
+
+
+def test_more_than_2_to_31_elements():
+    """The last rows of 270000 x 8192 equal the same rows alone."""
+    T, H = 270000, 8192
+    _log("2.2e9 elements")
+    g = torch.Generator(device="cuda").manual_seed(12)
+    r = torch.empty(T, H, dtype=BF16, device="cuda").normal_(generator=g)
+    y = torch.empty(T, H, dtype=BF16, device="cuda").normal_(generator=g)
+    w = 1 + 0.1 * torch.randn(H, generator=g, device="cuda")
+    out, n, _, _ = moe.moe_block_norm(r, y, post_weight=w, pre_weight=w)
+    few = moe.moe_block_norm(r[-600:].clone(), y[-600:].clone(), post_weight=w, pre_weight=w)
+    assert torch.equal(out[-600:], few[0]) and torch.equal(n[-600:], few[1])
+    assert torch.equal(out[:600], moe.moe_block_norm(r[:600], y[:600], post_weight=w, pre_weight=w)[0])
