@@ -189,8 +189,8 @@ __device__ __forceinline__ void wave_lds_order() {
 //
 // SHARED: the workgroup's waves have tiles of their own and the same k, so
 // each loads the x of one step of a block for all of them; otherwise they
-// split k and each loads its own.
-template <bool E4M3, int MODE, int ROWS, bool SHARED>
+// split k and each loads its own.  TAIL: k may end inside a block.
+template <bool E4M3, int MODE, int ROWS, bool SHARED, bool TAIL>
 __device__ __forceinline__ void multiply_rows(const MatvecArgs& a, const Share& sh, int m0, int lane, int wave,
                                               u32x4_t* lds, u32x4_t* x_lds, f32x4_t (&acc)[(ROWS + 15) / 16][kNT]) {
     constexpr bool kXFirst = MODE != kFolded;
@@ -443,7 +443,7 @@ __device__ __forceinline__ void multiply_rows(const MatvecArgs& a, const Share& 
         }
     }
     // What is left, one step at a time and straight into fragments; the last may end inside (K % 128 != 0).
-    if (sh.first + kBlock * sh.blocks >= sh.last) return;
+    if constexpr (!TAIL) return;
     int64_t frag_row[MT];
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) frag_row[mt] = x_row(mt * 16 + lr);
@@ -508,7 +508,7 @@ __device__ __forceinline__ void multiply_rows(const MatvecArgs& a, const Share& 
 // columns of its own; otherwise they split the k range of one tile.  MAXROWS:
 // rows that one pass over the weights serves; an expert with more takes
 // several.
-template <bool E4M3, int MODE, int MAXROWS, bool SHARED>
+template <bool E4M3, int MODE, int MAXROWS, bool SHARED, bool TAIL>
 __global__ __launch_bounds__(kMaxThreads, 2) void expert_matvec_kernel(MatvecArgs a) {
     // the operand whose scale is per row of its own goes second: a lane's four
     // sums then share that row
@@ -546,7 +546,7 @@ __global__ __launch_bounds__(kMaxThreads, 2) void expert_matvec_kernel(MatvecArg
         constexpr int ROWS = decltype(rows_const)::value;
         constexpr int MT = (ROWS + 15) / 16;
         f32x4_t acc[MT][kNT] = {};
-        multiply_rows<E4M3, MODE, ROWS, SHARED>(a, sh, m0, lane, wave, mine, x_lds, acc);
+        multiply_rows<E4M3, MODE, ROWS, SHARED, TAIL>(a, sh, m0, lane, wave, mine, x_lds, acc);
         wave_lds_order();
         float* sums = reinterpret_cast<float*>(mine);
         // the first operand's rows run along a lane's sums, the second's along the lanes
@@ -589,7 +589,7 @@ __global__ __launch_bounds__(kMaxThreads, 2) void expert_matvec_kernel(MatvecArg
     }
 }
 
-template <bool E4M3, int MODE, int MAXROWS>
+template <bool E4M3, int MODE, int MAXROWS, bool TAIL>
 hipError_t launch_rows(const MatvecArgs& a, int64_t experts, hipStream_t stream) {
     const int64_t tiles = (a.N + kCols - 1) / kCols;
     const int blocks = a.K / (kStep * kBlock);
@@ -598,25 +598,36 @@ hipError_t launch_rows(const MatvecArgs& a, int64_t experts, hipStream_t stream)
     if (tiles * experts >= 2048 || blocks < 2) {
         const dim3 grid(static_cast<unsigned>((tiles + kSharedWaves - 1) / kSharedWaves),
                         static_cast<unsigned>(experts));
-        hipLaunchKernelGGL((expert_matvec_kernel<E4M3, MODE, MAXROWS, true>), grid, dim3(kSharedWaves * kWave),
+        hipLaunchKernelGGL((expert_matvec_kernel<E4M3, MODE, MAXROWS, true, TAIL>), grid, dim3(kSharedWaves * kWave),
                            lds_bytes(true, MAXROWS, kSharedWaves), stream, a);
     } else {
         int split = 2;
         while (split < kMaxSplit && tiles * experts * split < 4096 && blocks >= 2 * split) split *= 2;
-        hipLaunchKernelGGL((expert_matvec_kernel<E4M3, MODE, MAXROWS, false>),
+        hipLaunchKernelGGL((expert_matvec_kernel<E4M3, MODE, MAXROWS, false, TAIL>),
                            dim3(static_cast<unsigned>(tiles), static_cast<unsigned>(experts)), dim3(split * kWave),
                            lds_bytes(false, MAXROWS, split), stream, a);
     }
     return hipGetLastError();
 }
 
+// The rows that a pass over the weights serves.  No expert has more rows than
+// there are, and of many experts few have many times the average; fewer rows
+// take less LDS and fewer registers (128 rows over 32 experts: 83 us with 16,
+// 95 us with 32), but an expert with more reads its weights again (512 rows
+// over 32: 77 us with 16, 65 us with 32).  k that ends inside a block takes 16:
+// the code for its last steps costs the registers of a wave in four (65
+// against 69 us without it).  So do fp32 scales of 32 channels, whose sums of
+// 32 rows would not fit.
 template <bool E4M3, int MODE>
 hipError_t launch_matvec(const MatvecArgs& a, hipStream_t stream) {
     const int64_t experts = a.E < a.num_rows ? a.E : a.num_rows;
-    // no expert has more rows than there are; of many experts few have four times the average
-    if (a.num_rows <= 8 || a.num_rows <= 2 * a.E) return launch_rows<E4M3, MODE, 8>(a, experts, stream);
-    // fp32 scales of 32 channels take registers for four sums at a time: 32 rows of them do not fit
-    return launch_rows<E4M3, MODE, MODE == kF32Group32 ? 16 : 32>(a, experts, stream);
+    if (a.K % (kStep * kBlock) != 0) return launch_rows<E4M3, MODE, 16, true>(a, experts, stream);
+    if (a.num_rows <= 8 || a.num_rows <= 2 * static_cast<int64_t>(a.E))
+        return launch_rows<E4M3, MODE, 8, false>(a, experts, stream);
+    if constexpr (MODE != kF32Group32)
+        if (a.num_rows > 16 && a.num_rows > 8 * static_cast<int64_t>(a.E))
+            return launch_rows<E4M3, MODE, 32, false>(a, experts, stream);
+    return launch_rows<E4M3, MODE, 16, false>(a, experts, stream);
 }
 
 }  // namespace
