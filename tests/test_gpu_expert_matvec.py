@@ -67,13 +67,13 @@ def _want(s):
         t = s["row_token"].long()
         ok = (t >= 0) & (t < x.shape[0])
         x = torch.where(ok[:, None], x[t.clamp(0, max(0, x.shape[0] - 1))], 0.0)
-    out = torch.full((s["rows"], N), float("nan"), dtype=torch.float64)
+    out = torch.full((s["rows"], N), float("nan"), dtype=torch.float64, device=x.device)
     mag = torch.zeros_like(out)
     off = s["expert_offsets"].tolist()
     for e in range(E):
         if off[e + 1] <= off[e]:
             continue
-        w = VALUES[torch.stack([s["w"][e] & 15, s["w"][e] >> 4], 2).view(N, 2 * K2).long()]
+        w = VALUES.to(x.device)[torch.stack([s["w"][e] & 15, s["w"][e] >> 4], 2).view(N, 2 * K2).long()]
         sf = s["w_sf"][e].double()
         if s["w_sf"].dtype == torch.uint8:
             sf = torch.pow(2.0, sf - 127)
@@ -136,6 +136,36 @@ def test_rows_of_one_matrix(rows, x, group, sf):
     got = _call(s).double().cpu()
     bound = (512 + 16) * EPS32 * mag
     assert ((got - want).abs() <= bound + EPS16 * (want.abs() + bound)).all()
+
+
+@pytest.mark.parametrize("counts", [[2, 3, 1, 2], [4, 12, 0, 4], [17, 1, 0, 2], [5, 33, 9, 16], [70, 4, 8, 1]])
+@pytest.mark.parametrize("x,group,sf", FORMATS)
+def test_many_columns(counts, x, group, sf):
+    """So many tiles that each wave has one of its own: several blocks of k, few rows and many, the last tiles past
+    the columns."""
+    for K in (1024, 1536):
+        _log(f"many columns {counts} {x} {group} {sf} K={K}")
+        s = _inputs(counts, 16400, K, x, group, sf, seed=sum(counts), tokens=9 if K == 1536 else None)
+        d = {k: v.cuda() if isinstance(v, torch.Tensor) else v for k, v in s.items()}
+        want, mag = _want(d)
+        got = _call(s).double()
+        bound = (K + 16) * EPS32 * mag
+        assert ((got - want).abs() <= bound + EPS16 * (want.abs() + bound)).all()
+
+
+@pytest.mark.parametrize("x,group,sf", FORMATS)
+@pytest.mark.parametrize("K", [512, 1024, 2048, 4096, 2176])
+def test_few_columns(x, group, sf, K):
+    """So few tiles that waves split k, in one, two and four shares, even and not."""
+    for counts in ([1], [3, 0, 6], [20, 2], [40]):
+        for N in (33, 2100):
+            _log(f"few columns {counts} {x} {group} {sf} K={K} N={N}")
+            s = _inputs(counts, N, K, x, group, sf, seed=K)
+            d = {k: v.cuda() if isinstance(v, torch.Tensor) else v for k, v in s.items()}
+            want, mag = _want(d)
+            got = _call(s).double()
+            bound = (K + 16) * EPS32 * mag
+            assert ((got - want).abs() <= bound + EPS16 * (want.abs() + bound)).all()
 
 
 @pytest.mark.parametrize("x", ["bf16", "e4m3"])
