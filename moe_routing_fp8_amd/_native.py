@@ -974,12 +974,11 @@ def moe_balance_loss(logits: torch.Tensor, topk_idx: torch.Tensor, score: str = 
     "sigmoid" divided by the row's sum."""
     stride, mode, S = _balance_inputs(logits, score, token_mask, seq_offsets)
     T, E = logits.shape
-    _need(topk_idx, torch.int64, 2, "topk_idx")
+    if topk_idx.dim() != 2:
+        raise ValueError(f"topk_idx: expected a 2-d tensor, got {tuple(topk_idx.shape)}")
     K = topk_idx.shape[1]
-    _shape(topk_idx, (T, K), "topk_idx")
     dev = logits.device
-    if topk_idx.device != dev:
-        _device(logits, topk_idx)
+    _need_out(topk_idx, torch.int64, (T, K), "topk_idx", dev)
     if out is None:
         with _alloc_on(stream):
             out = {"loss": torch.empty(S, device=dev), "counts": torch.empty((S, E), dtype=torch.int32, device=dev),
@@ -1028,37 +1027,36 @@ def moe_expert_matvec(x: torch.Tensor, w_codes: torch.Tensor, w_sf: torch.Tensor
     w_codes uint8 [E, N, K/2] (e2m1, as moe_expand_cast writes them; [N, K/2] for one matrix), w_sf uint8 (UE8M0) or
     fp32 [E, N, K/g] with g = 32 or 128; expert_offsets int32 [E+1] (None: one matrix, all rows); row_token int32
     [R] to read row r from x[row_token[r]] (None: R == X) -> bf16 [R, N].  Rows of no expert are not written."""
-    if x.dtype != torch.bfloat16 and x.dtype not in _FP8:
+    e4m3 = x.dtype != torch.bfloat16
+    if e4m3 and x.dtype not in _FP8:
         raise ValueError(f"x: expected bf16 or e4m3 codes, got {x.dtype}")
-    _need(x, x.dtype, 2, "x")
+    if x.dim() != 2 or not x.is_contiguous():
+        raise ValueError(f"x: expected a contiguous 2-d tensor, got {tuple(x.shape)} strides {x.stride()}")
+    dev = x.device
+    X, K = x.shape
     if w_codes.dim() == 2:
         w_codes, w_sf = w_codes.unsqueeze(0), w_sf.unsqueeze(0)
-    _need(w_codes, torch.uint8, 3, "w_codes")
-    X, K = x.shape
-    E, N = w_codes.shape[:2]
-    _shape(w_codes, (E, N, K // 2), "w_codes")
-    ue8m0 = w_sf.dtype == torch.uint8
-    _need(w_sf, torch.uint8 if ue8m0 else torch.float32, 3, "w_sf")
+    if w_codes.dim() != 3 or w_sf.dim() != 3:
+        raise ValueError(f"w_codes, w_sf: expected [E, N, ..] tensors, got {tuple(w_codes.shape)}, {tuple(w_sf.shape)}")
+    E, N, _ = w_codes.shape
+    _need_out(w_codes, torch.uint8, (E, N, K // 2), "w_codes", dev)
     G = w_sf.shape[2]
-    _shape(w_sf, (E, N, G), "w_sf")
+    ue8m0 = w_sf.dtype == torch.uint8
+    _need_out(w_sf, torch.uint8 if ue8m0 else torch.float32, (E, N, G), "w_sf", dev)
     if G == 0 or K % G != 0:
         raise ValueError(f"w_sf: {G} scales for a row of {K} weights")
-    e4m3 = x.dtype != torch.bfloat16
     if e4m3 != (x_sf is not None):
         raise ValueError("x_sf: given with e4m3 rows, and only then")
-    if x_sf is not None:
-        _need(x_sf, torch.float32, 2, "x_sf")
-        _shape(x_sf, (X, K // 128), "x_sf")
+    if e4m3:
+        _need_out(x_sf, torch.float32, (X, K // 128), "x_sf", dev)
     if expert_offsets is not None:
-        _need(expert_offsets, torch.int32, 1, "expert_offsets")
-        _shape(expert_offsets, (E + 1,), "expert_offsets")
+        _need_out(expert_offsets, torch.int32, (E + 1,), "expert_offsets", dev)
     elif E != 1:
         raise ValueError("expert_offsets: required with more than one expert")
     R = X
     if row_token is not None:
-        _need(row_token, torch.int32, 1, "row_token")
-        R = row_token.shape[0]
-    dev = _device(x, w_codes, w_sf, x_sf, expert_offsets, row_token)
+        R = row_token.numel()
+        _need_out(row_token, torch.int32, (R,), "row_token", dev)
     if out is None:
         with _alloc_on(stream):
             out = torch.empty((R, N), dtype=torch.bfloat16, device=dev)

@@ -134,10 +134,11 @@ __device__ __forceinline__ bool find_expert(const MatvecArgs& a, int index, int 
 
 __device__ __forceinline__ u32x4_t u32x4(uint32_t a, uint32_t b, uint32_t c, uint32_t d) { return u32x4_t{a, b, c, d}; }
 
-struct __attribute__((packed, aligned(4))) Words4 {  // four words, 4-byte aligned
+// Four words and one of them at any alignment (a row of scale bytes starts anywhere).
+struct __attribute__((packed, aligned(1))) Words4 {
     uint32_t w[4];
 };
-struct __attribute__((packed, aligned(1))) Word {  // one word, any alignment
+struct __attribute__((packed, aligned(1))) Word {
     uint32_t w;
 };
 
@@ -443,65 +444,74 @@ __device__ __forceinline__ void multiply_rows(const MatvecArgs& a, const Share& 
             }
         }
     }
-    // What is left, one step at a time and straight into fragments; the last may end inside (K % 128 != 0).
+    // What is left, less than a block, straight into fragments: all of its loads first.  The last step may end inside
+    // (K % 128 != 0).
     if constexpr (!TAIL) return;
+    const int base = sh.first + kBlock * sh.blocks;
     int64_t frag_row[MT];
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) frag_row[mt] = x_row(mt * 16 + lr);
-    for (int step = sh.first + kBlock * sh.blocks; step < sh.last; ++step) {
-        const int k0 = step * kStep;
-        u32x4_t w[kNT], x[MT][XV] = {};
-        float ws[kNT][4], xs[MT] = {};
+    u32x4_t w[kBlock][kNT], x[kBlock][MT][XV] = {};
+    float ws[kBlock][kNT][4], xs[kBlock][MT] = {};
+#pragma unroll
+    for (int j = 0; j < kBlock; ++j) {
+        const int step = base + j, k0 = step * kStep;
+        if (step >= sh.last) break;
         const bool in = k0 + q * 32 < K;
 #pragma unroll
         for (int nt = 0; nt < kNT; ++nt) {
             const int64_t n = row_e + min(sh.n0 + nt * 16 + lr, a.N - 1);
-            w[nt] = u32x4(0, 0, 0, 0);
-            if (in) w[nt] = *reinterpret_cast<const u32x4_t*>(a.codes + n * (K / 2) + k0 / 2 + q * 16);
+            w[j][nt] = u32x4(0, 0, 0, 0);
+            if (in) w[j][nt] = *reinterpret_cast<const u32x4_t*>(a.codes + n * (K / 2) + k0 / 2 + q * 16);
             if constexpr (MODE == kFolded) {
-                ws[nt][0] = 1.0f;
+                ws[j][nt][0] = 1.0f;
                 if (in)
-                    ws[nt][0] = __uint_as_float(
+                    ws[j][nt][0] = __uint_as_float(
                         static_cast<uint32_t>(
                             static_cast<const uint8_t*>(a.sf)[n * (K / a.group) + (k0 + q * 32) / a.group])
                         << 23);
             } else if constexpr (MODE == kF32Group128) {
-                ws[nt][0] = static_cast<const float*>(a.sf)[n * (K / 128) + step];
+                ws[j][nt][0] = static_cast<const float*>(a.sf)[n * (K / 128) + step];
             } else {
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    ws[nt][i] = k0 + i * 32 < K ? static_cast<const float*>(a.sf)[n * (K / 32) + 4 * step + i] : 0.0f;
+                    ws[j][nt][i] =
+                        k0 + i * 32 < K ? static_cast<const float*>(a.sf)[n * (K / 32) + 4 * step + i] : 0.0f;
             }
         }
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
             if (frag_row[mt] < 0) continue;
             if constexpr (E4M3) {
-                xs[mt] = a.x_sf[frag_row[mt] * (K / 128) + step];
+                xs[j][mt] = a.x_sf[frag_row[mt] * (K / 128) + step];
                 const uint8_t* p = static_cast<const uint8_t*>(a.x) + frag_row[mt] * K + k0;
                 if constexpr (MODE == kF32Group32) {
                     u32x2_t c[4];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) c[i] = *reinterpret_cast<const u32x2_t*>(p + 32 * i + 8 * q);
-                    x[mt][0] = u32x4(c[0].x, c[0].y, c[1].x, c[1].y);
-                    x[mt][1] = u32x4(c[2].x, c[2].y, c[3].x, c[3].y);
+                    x[j][mt][0] = u32x4(c[0].x, c[0].y, c[1].x, c[1].y);
+                    x[j][mt][1] = u32x4(c[2].x, c[2].y, c[3].x, c[3].y);
                 } else {
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) x[mt][i] = *reinterpret_cast<const u32x4_t*>(p + 32 * q + 16 * i);
+                    for (int i = 0; i < 2; ++i) x[j][mt][i] = *reinterpret_cast<const u32x4_t*>(p + 32 * q + 16 * i);
                 }
             } else {
                 const uint16_t* p = static_cast<const uint16_t*>(a.x) + frag_row[mt] * K + k0;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int k = MODE == kF32Group32 ? 32 * i + 8 * q : 32 * q + 8 * i;
-                    if (k0 + k < K) x[mt][i] = *reinterpret_cast<const u32x4_t*>(p + k);
+                    if (k0 + k < K) x[j][mt][i] = *reinterpret_cast<const u32x4_t*>(p + k);
                 }
             }
         }
-        bf16x8_t wf[kNT][4];
-        unpack_codes(wf, w, ws);
+    }
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt) multiply(wf, ws, x[mt], xs[mt], acc[mt]);
+    for (int j = 0; j < kBlock; ++j) {
+        if (base + j >= sh.last) break;
+        bf16x8_t wf[kNT][4];
+        unpack_codes(wf, w[j], ws[j]);
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) multiply(wf, ws[j], x[j][mt], xs[j][mt], acc[mt]);
     }
 }
 
@@ -525,18 +535,13 @@ __global__ __launch_bounds__(kMaxThreads, 2) void expert_matvec_kernel(MatvecArg
     const int split = SHARED ? 1 : waves, part = SHARED ? 0 : wave;
     sh.n0 = (SHARED ? blockIdx.x * waves + wave : blockIdx.x) * kCols;  // may be past N: then nothing is written
     const int steps = (a.K + kStep - 1) / kStep;
-    // blocks need whole steps and, for the scales' words, rows of whole words
-    const int blocks = a.K % kStep == 0 ? steps / kBlock : 0;
+    const int blocks = a.K / (kStep * kBlock);
     if (a.x_rows == 0) {
         sh.first = sh.blocks = sh.last = 0;
-    } else if (blocks > 0) {
+    } else {  // the last wave also takes what is left after the blocks
         sh.first = blocks * part / split * kBlock;
         sh.blocks = blocks * (part + 1) / split - blocks * part / split;
         sh.last = part == split - 1 ? steps : sh.first + kBlock * sh.blocks;
-    } else {
-        sh.first = steps * part / split;
-        sh.last = steps * (part + 1) / split;
-        sh.blocks = 0;
     }
 
     // Leaves the wave's sums in LDS, adds the shares of the tile's waves in order and writes the rows.
