@@ -465,8 +465,7 @@ moe_status swiglu_cast(const uint16_t* gate_up_bf16, int64_t num_rows, int32_t i
  *                where that is contiguous.
  * post_rstd,     fp32 [T]: the two factors rsqrt(mean + eps), which the
  * pre_rstd       backward pass reads, or NULL.
- * Any alignment of the element type; 16-byte aligned rows with H a multiple of
- * 8 run on 16-byte accesses.
+ * Any alignment of the element type.
  */
 moe_status moe_block_norm(const void* residual, int64_t residual_stride, int32_t residual_dtype, const void* y,
                           int64_t y_stride, int32_t act_dtype, int64_t num_tokens, int32_t hidden,

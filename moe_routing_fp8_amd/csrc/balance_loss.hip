@@ -13,9 +13,8 @@
 // Forward, one to three launches.  The tokens are cut into chunks of consecutive
 // tokens, one workgroup each; 16 lanes (64 above 256 experts) hold a token's
 // whole row of logits in registers and keep their running sums of p there
-// too.  A chunk may meet
-// several sequences: each (chunk, sequence) piece is summed over the
-// workgroup's waves in a fixed order and written to a slot of its own,
+// too.  A chunk may meet several sequences: each (chunk, sequence) piece is
+// summed over the workgroup's waves in a fixed order and written to a slot of its own,
 // number chunk + sequence (along the pieces in token order either index
 // grows, so no two pieces share a slot, and a sequence's slots are
 // consecutive).  Then each sequence's slots are added in a fixed order: by one
@@ -23,6 +22,13 @@
 // workgroups that take a few columns each, with the loss in a third launch.  A
 // batch of one chunk takes its losses in the first launch.
 // No floating atomics: the results do not depend on timing.
+//
+// Kernel traces (sums, slots, [loss], gradient), beside a launch of nothing at 3.8 us:
+//   32768 x 256 fp32, one sequence      10.9 + 4.8 + 2.4 + 12.3 us; the sums read 3.3 TB/s: as many
+//                                       steps of the row reductions and exponentials as loads
+//   4096 x 256 bf16, eight sequences    7.9 + 5.5 + 5.4 us, latency
+//   10007 x 61 fp32, 311 sequences      9.0 + 3.8 + 5.8 us, latency
+//   64 x 16 fp32, one sequence          4.4 us in one launch, latency
 // Backward, one launch: the same lanes per token read the row again, with the
 // sequence's counts in registers.
 //

@@ -14,6 +14,13 @@
 // over rows: a workgroup walks over rows with a stride, keeps its columns'
 // running sums in registers, and writes them once; a second launch adds the
 // workgroups' sums in order.
+//
+// Bound by the bytes of the rows; kernel traces:
+//   forward, 4096 x 7168, bf16                     48.5 us  4.8 TB/s
+//   backward, 4096 x 7168, fp32 r and bf16 y       104.8 + 5.4 us  4.8 TB/s
+//   backward, 1021 x 2049, bf16 (cached)           16.4 + 3.9 us: the three dependent sums of two rows in turn
+//   forward, one row of 7168, bf16                 3.9 us: a launch and the two dependent sums
+// A large copy runs at 5.2 TB/s.
 #include <hip/hip_runtime.h>
 
 #include "api_common.hpp"
@@ -41,7 +48,8 @@ __device__ __forceinline__ float rsqrt_f32(float v) {
 // Rows of more bytes than this in all are read and written past the caches
 // (half of the 256 MB of Infinity Cache: what is larger finds nothing there
 // when it comes round again).  4096 x 7168 bf16: 48.0 us against 54.8.  The
-// backward pass streams its stores only (119.1 us against 121.8; with
+// backward pass streams its stores only (119.1 us against 121.8 before its
+// rows took one shape of access for all alignments, which made it 110; with
 // streaming loads 131).
 constexpr int64_t kStreamBytes = int64_t{128} << 20;
 

@@ -5,9 +5,19 @@
 //
 // Rows are grouped by expert (expert_offsets).  Up to some 64 rows per expert
 // the weights' bytes bound the time, so the kernel is built around one pass
-// over them: a wave reads 16 weight rows at a time, each lane 16 bytes (32
-// codes) of one row, and every fragment it unpacks feeds the matrix cores
-// for up to MT * 16 rows of x.
+// over them: a wave owns 32 weight rows (output columns) and walks along k in
+// steps of 128; every fragment of codes that it unpacks meets up to MAXROWS
+// (8, 16 or 32) rows of x in the matrix cores.
+//
+// Measured, from kernel traces (weights, scales, rows and results over the time):
+//   one token's 8 experts, 7168 -> 4096, UE8M0 scales, bf16 x   25 us    5.0 TB/s
+//   128 rows, 32 experts, 7168 -> 4096, UE8M0 scales, e4m3 x    80 to 88 us, 5.6 to 6.1 TB/s
+//   512 rows, 32 experts, 2048 -> 7168, fp32 scales, bf16 x     62 to 65 us, 4.0 to 4.2 TB/s
+//   one row, one expert, 2048 -> 7168, UE8M0 scales, bf16 x     5.1 us   (latency: a launch and two blocks of k)
+// A bare streaming read of such arrays reaches 6.1 to 7.0 TB/s.  With few rows
+// the start and the drain of a launch of one round of waves bound it; with 16
+// and more rows the registers, which allow two waves a SIMD and so bound the
+// loads in flight while the matrix cores and the conversions work.
 //
 // Products.  An e2m1 value is exact in bf16, and so is an e4m3 value of x, so
 // both go through the bf16 matrix instruction with exact products and fp32
@@ -27,7 +37,10 @@
 //   - fp32 scales per 32 k: instruction i must cover one group, k = 32 i +
 //     8 q + (0..7); four lane-row swaps transpose the dwords over the lane
 //     quarters.
-// The workgroup's waves split k; their sums meet in LDS in a fixed order.
+// Workgroups.  Where there is a tile of columns for every wave the chip holds,
+// a workgroup's four waves take four tiles and share their rows of x (SHARED);
+// with fewer tiles the workgroup's waves split the k of one, and their sums
+// meet in LDS in a fixed order.
 #include <hip/hip_runtime.h>
 
 #include <type_traits>
