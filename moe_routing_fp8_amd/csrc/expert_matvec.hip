@@ -237,7 +237,7 @@ __device__ __forceinline__ void multiply_rows(const MatvecArgs& a, const Share& 
     // x: load i's row i * kRowsPerLoad + lane / kChunks
     auto x_row = [&](int m) -> int64_t {
         int64_t r = -1;
-        if (m0 + m < sh.rows && m < ROWS) r = a.row_token != nullptr ? a.row_token[sh.row0 + m0 + m] : sh.row0 + m0 + m;
+        if (m < sh.rows - m0 && m < ROWS) r = a.row_token != nullptr ? a.row_token[sh.row0 + m0 + m] : sh.row0 + m0 + m;
         return r < a.x_rows ? r : -1;
     };
     const uint8_t* xp[XI];
@@ -531,7 +531,7 @@ __device__ __forceinline__ void multiply_rows(const MatvecArgs& a, const Share& 
 // A workgroup is blockDim / 64 waves.  SHARED: each has a tile of kCols output
 // columns of its own; otherwise they split the k range of one tile.  MAXROWS:
 // rows that one pass over the weights serves; an expert with more takes
-// several.
+// several, which the grid's z shares out.
 template <bool E4M3, int MODE, int MAXROWS, bool SHARED, bool TAIL>
 __global__ __launch_bounds__(kMaxThreads, 2) void expert_matvec_kernel(MatvecArgs a) {
     // the operand whose scale is per row of its own goes second: a lane's four
@@ -583,7 +583,7 @@ __global__ __launch_bounds__(kMaxThreads, 2) void expert_matvec_kernel(MatvecArg
             __syncthreads();
         for (int i = part * kWave + lane; i < ROWS * kCols; i += split * kWave) {
             const int m = i / kCols, n = i % kCols;
-            if (m0 + m >= sh.rows || sh.n0 + n >= a.N) continue;
+            if (m >= sh.rows - m0 || sh.n0 + n >= a.N) continue;
             float v = 0.0f;
             for (int w = 0; w < split; ++w) v += tile[w * (kLdsWave * 4) + m * kPitch + n];
             const int64_t r = sh.row0 + m0 + m;
@@ -594,8 +594,10 @@ __global__ __launch_bounds__(kMaxThreads, 2) void expert_matvec_kernel(MatvecArg
             a.out[r * a.N + sh.n0 + n] = bf16_bits(v);
         }
     };
-    for (int m0 = 0; m0 < sh.rows; m0 += MAXROWS) {
-        if (m0 > 0) __syncthreads();  // the sums and operands in LDS have been read
+    const int64_t first = int64_t{blockIdx.z} * MAXROWS, stride = int64_t{gridDim.z} * MAXROWS;
+    for (int64_t m = first; m < sh.rows; m += stride) {
+        if (m > first) __syncthreads();  // the sums and operands in LDS have been read
+        const int m0 = static_cast<int>(m);
         const int rows = sh.rows - m0;
         if (!E4M3 && MAXROWS <= 8 && rows <= 4)
             run(std::integral_constant<int, 4>{}, m0);
@@ -615,17 +617,24 @@ hipError_t launch_rows(const MatvecArgs& a, int64_t experts, hipStream_t stream)
     // A wave for each tile where that fills the eight places for waves of every compute unit (their registers allow
     // two a SIMD); else the waves of a workgroup split k, as far as there is a block of steps for each, until all
     // places are taken.  One token's eight experts, 1024 tiles: 25.1 us split in two, 28.5 us in four (two rounds).
+    // Places still free take an expert's passes side by side (72 rows of one matrix, 1568 -> 4096: 9.3 us, 27.3 us one
+    // after another); an expert with fewer passes leaves its spare workgroups at once.
+    auto passes = [&](int64_t waves) {
+        const int64_t most = (a.num_rows + MAXROWS - 1) / MAXROWS, free = kWavePlaces / waves;
+        return static_cast<unsigned>(free < 1 ? 1 : free < most ? free : most);
+    };
     if (tiles * experts >= kWavePlaces || blocks < 2) {
         const dim3 grid(static_cast<unsigned>((tiles + kSharedWaves - 1) / kSharedWaves),
-                        static_cast<unsigned>(experts));
+                        static_cast<unsigned>(experts), passes(tiles * experts));
         hipLaunchKernelGGL((expert_matvec_kernel<E4M3, MODE, MAXROWS, true, TAIL>), grid, dim3(kSharedWaves * kWave),
                            lds_bytes(true, MAXROWS, kSharedWaves), stream, a);
     } else {
         int split = 2;
         while (split < kMaxSplit && tiles * experts * split < kWavePlaces && blocks >= 2 * split) split *= 2;
         hipLaunchKernelGGL((expert_matvec_kernel<E4M3, MODE, MAXROWS, false, TAIL>),
-                           dim3(static_cast<unsigned>(tiles), static_cast<unsigned>(experts)), dim3(split * kWave),
-                           lds_bytes(false, MAXROWS, split), stream, a);
+                           dim3(static_cast<unsigned>(tiles), static_cast<unsigned>(experts),
+                                passes(tiles * experts * split)),
+                           dim3(split * kWave), lds_bytes(false, MAXROWS, split), stream, a);
     }
     return hipGetLastError();
 }

@@ -168,6 +168,20 @@ def test_few_columns(x, group, sf, K):
             assert ((got - want).abs() <= bound + EPS16 * (want.abs() + bound)).all()
 
 
+@pytest.mark.parametrize("x,group,sf", FORMATS)
+@pytest.mark.parametrize("N,K", [(2050, 2048), (8200, 512), (130, 640)])
+def test_more_rows_than_one_pass_takes(x, group, sf, N, K):
+    """An expert's passes side by side and in turn, beside experts with few rows or none."""
+    for counts in ([72], [500], [300, 0, 9]):
+        _log(f"passes {counts} {x} {group} {sf} K={K} N={N}")
+        s = _inputs(counts, N, K, x, group, sf, seed=N)
+        d = {k: v.cuda() if isinstance(v, torch.Tensor) else v for k, v in s.items()}
+        want, mag = _want(d)
+        got = _call(s).double()
+        bound = (K + 16) * EPS32 * mag
+        assert ((got - want).abs() <= bound + EPS16 * (want.abs() + bound)).all()
+
+
 @pytest.mark.parametrize("x", ["bf16", "e4m3"])
 def test_expert_loads(x):
     """Experts without rows at either end and between, one expert with everything, rows of no expert around."""
