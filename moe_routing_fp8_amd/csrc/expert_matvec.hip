@@ -213,7 +213,7 @@ __device__ __forceinline__ void multiply_rows(const MatvecArgs& a, const Share& 
     constexpr int kChunks = E4M3 ? 8 : 16;             // 16-byte chunks of a row of x in a step
     constexpr int kRowsPerLoad = kWave / kChunks;
     constexpr int XI = (ROWS + kRowsPerLoad - 1) / kRowsPerLoad;
-    constexpr int kAhead = SHARED ? 1 : ROWS > 16 ? 2 : kBlock;  // steps of x in the wave's registers
+    constexpr int kAhead = SHARED ? 1 : kBlock;  // steps of x in the wave's registers
     constexpr int kStepX = ROWS * kChunks;             // LDS of a step's x
     constexpr int XV = E4M3 ? 2 : 4;                   // 16-byte vectors of a lane's fragments of one step
     const int lr = lane & 15, q = lane >> 4;
@@ -623,12 +623,13 @@ hipError_t launch_rows(const MatvecArgs& a, int64_t experts, hipStream_t stream)
         const int64_t most = (a.num_rows + MAXROWS - 1) / MAXROWS, free = kWavePlaces / waves;
         return static_cast<unsigned>(free < 1 ? 1 : free < most ? free : most);
     };
-    if (tiles * experts >= kWavePlaces || blocks < 2) {
+    constexpr bool kManyTiles = MAXROWS > 16;  // the caller's rule
+    if (kManyTiles || tiles * experts >= kWavePlaces || blocks < 2) {
         const dim3 grid(static_cast<unsigned>((tiles + kSharedWaves - 1) / kSharedWaves),
                         static_cast<unsigned>(experts), passes(tiles * experts));
         hipLaunchKernelGGL((expert_matvec_kernel<E4M3, MODE, MAXROWS, true, TAIL>), grid, dim3(kSharedWaves * kWave),
                            lds_bytes(true, MAXROWS, kSharedWaves), stream, a);
-    } else {
+    } else if constexpr (!kManyTiles) {
         int split = 2;
         while (split < kMaxSplit && tiles * experts * split < kWavePlaces && blocks >= 2 * split) split *= 2;
         hipLaunchKernelGGL((expert_matvec_kernel<E4M3, MODE, MAXROWS, false, TAIL>),
@@ -643,7 +644,9 @@ hipError_t launch_rows(const MatvecArgs& a, int64_t experts, hipStream_t stream)
 // there are, and of many experts few have many times the average; fewer rows
 // take less LDS and fewer registers (128 rows over 32 experts: 83 us with 16,
 // 95 us with 32), but an expert with more reads its weights again (512 rows
-// over 32: 77 us with 16, 65 us with 32).  k that ends inside a block takes 16:
+// over 32: 77 us with 16, 65 us with 32), unless there are places for its
+// passes side by side (200 rows of one matrix, 7168 -> 512: 12.1 us with 16,
+// 18.0 us with 32).  k that ends inside a block takes 16:
 // the code for its last steps costs the registers of a wave in four (65
 // against 69 us without it).  So do fp32 scales of 32 channels, whose sums of
 // 32 rows would not fit.
@@ -654,7 +657,8 @@ hipError_t launch_matvec(const MatvecArgs& a, hipStream_t stream) {
     if (a.num_rows <= 8 || a.num_rows <= 2 * static_cast<int64_t>(a.E))
         return launch_rows<E4M3, MODE, 8, false>(a, experts, stream);
     if constexpr (MODE != kF32Group32)
-        if (a.num_rows > 16 && a.num_rows > 8 * static_cast<int64_t>(a.E))
+        if (a.num_rows > 16 && a.num_rows > 8 * static_cast<int64_t>(a.E) &&
+            (a.N + kCols - 1) / kCols * experts >= kWavePlaces)
             return launch_rows<E4M3, MODE, 32, false>(a, experts, stream);
     return launch_rows<E4M3, MODE, 16, false>(a, experts, stream);
 }
