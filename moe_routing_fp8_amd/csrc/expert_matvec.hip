@@ -46,18 +46,21 @@
 #include <type_traits>
 
 #include "api_common.hpp"
+#include "expert_matvec_lds.hpp"
 #include "math_device.hpp"
 #include "moe_fp8.h"
 
 namespace moe {
 namespace {
 
+using namespace matvec;
+
 typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
 typedef float f32x4_t __attribute__((ext_vector_type(4)));
 
 constexpr int kStep = 128;  // k per step of a wave
-constexpr int kMaxSplit = 4;  // waves that share a tile's k range
+static_assert(kLanes == kWave, "LDS layout");
 constexpr int kMaxThreads = kMaxSplit * kWave;
 constexpr int64_t kWavePlaces = 8 * 256;
 enum ScaleMode { kFolded = 0, kF32Group128 = 1, kF32Group32 = 2 };
@@ -164,25 +167,6 @@ struct Share {
     int first, blocks, last;
 };
 
-constexpr int kNT = 2;             // 16-column tiles of a wave
-constexpr int kCols = kNT * 16;
-constexpr int kBlock = 4;          // steps of a block: one 16-byte load of scales, and the depth of the loads in flight
-constexpr int kPair = 2;           // steps whose codes are loaded together: a row's 128 bytes, one cache line
-constexpr int kPitch = kCols + 1;  // floats of a row of sums in LDS
-constexpr int kSharedWaves = kBlock;  // waves of a workgroup that shares its x: one for each step of a block
-
-// LDS in 16-byte units.  Of each wave: codes of two steps, scales of a block
-// (kF32Group32: of a step), and its x of a step (private) or the workgroup's
-// x of a block (shared).  After the loop the sums of up to `rows` rows lie there.
-constexpr int kLdsCodes = kNT * kPair * kWave;
-constexpr int kLdsScales = kCols;
-constexpr int lds_x(bool shared, int rows) { return rows * 16 * (shared ? kBlock : 1); }
-constexpr int lds_wave(bool shared, int rows) { return kLdsCodes + kLdsScales + (shared ? 0 : lds_x(false, rows)); }
-constexpr size_t lds_bytes(bool shared, int rows, int waves) {
-    return sizeof(u32x4_t) * (static_cast<size_t>(waves) * lds_wave(shared, rows) + (shared ? lds_x(true, rows) : 0));
-}
-static_assert(32 * kPitch * 4 <= lds_wave(true, 32) * 16, "a wave's sums fit where its operands were");
-
 // Keeps the compiler from moving LDS accesses of one lane across those of
 // others that it has to stay behind; the hardware runs a wave's in order.
 __device__ __forceinline__ void wave_lds_order() {
@@ -198,17 +182,18 @@ __device__ __forceinline__ void wave_lds_order() {
 // the address unit four times as long, and one that takes half a cache line
 // leaves the next step's to wait in the cache for the line on its way; either
 // bounded the kernel (as did one byte of scales per lane and step).  The wave's own corner of LDS then turns the data
-// into fragments: lane (lr, q) reads row lr.  The 16-byte chunks of a row are
-// stored at (chunk XOR row), which spreads the eight rows that one LDS clock
-// serves over all banks.
+// into fragments: lane (lr, q) reads row lr (of x_unit's).  The
+// 16-byte chunks of a row are stored at (chunk XOR row), which spreads the
+// eight rows that one LDS clock serves over all banks.
 //
 // SHARED: the workgroup's waves have tiles of their own and the same k, so
 // each loads the x of one step of a block for all of them; otherwise they
 // split k and each loads its own.  TAIL: k may end inside a block.
-template <bool E4M3, int MODE, int ROWS, bool SHARED, bool TAIL>
+template <bool E4M3, int MODE, int MAXROWS, int ROWS, bool SHARED, bool TAIL>
 __device__ __forceinline__ void multiply_rows(const MatvecArgs& a, const Share& sh, int m0, int lane, int wave,
                                               u32x4_t* lds, u32x4_t* x_lds, f32x4_t (&acc)[(ROWS + 15) / 16][kNT]) {
     constexpr bool kXFirst = MODE != kFolded;
+    static_assert((ROWS & (ROWS - 1)) == 0 && ROWS <= MAXROWS, "rows of a pass");
     constexpr int MT = (ROWS + 15) / 16;
     constexpr int kChunks = E4M3 ? 8 : 16;             // 16-byte chunks of a row of x in a step
     constexpr int kRowsPerLoad = kWave / kChunks;
@@ -234,7 +219,7 @@ __device__ __forceinline__ void multiply_rows(const MatvecArgs& a, const Share& 
         }
     const uint8_t* sp = static_cast<const uint8_t*>(a.sf) + (row_e + min(sh.n0 + lane % kCols, a.N - 1)) *
                                                                (K / a.group) * (MODE == kFolded ? 1 : 4);
-    // x: load i's row i * kRowsPerLoad + lane / kChunks
+    // x: load i's row x_load_row(i)
     auto x_row = [&](int m) -> int64_t {
         int64_t r = -1;
         if (m < sh.rows - m0 && m < ROWS) r = a.row_token != nullptr ? a.row_token[sh.row0 + m0 + m] : sh.row0 + m0 + m;
@@ -243,11 +228,10 @@ __device__ __forceinline__ void multiply_rows(const MatvecArgs& a, const Share& 
     const uint8_t* xp[XI];
 #pragma unroll
     for (int i = 0; i < XI; ++i) {
-        const int m = i * kRowsPerLoad + lane / kChunks;
-        const int64_t r = x_row(m);
+        const int64_t r = x_row(x_load_row(kChunks, i, lane));
         xp[i] = r < 0 ? nullptr
                       : static_cast<const uint8_t*>(a.x) + r * (E4M3 ? K : 2 * static_cast<int64_t>(K)) +
-                            ((lane ^ m) & (kChunks - 1)) * 16;
+                            x_load_chunk(kChunks, i, lane) * 16;
     }
     const float* xsp[MT];  // scales of e4m3 row lr of each fragment
     if constexpr (E4M3)
@@ -434,19 +418,21 @@ __device__ __forceinline__ void multiply_rows(const MatvecArgs& a, const Share& 
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt) {
                     const int m = mt * 16 + lr;
-                    const u32x4_t* row = x_lds + (SHARED ? j * kStepX : 0) + m * kChunks;
+                    const u32x4_t* step_x = x_lds + (SHARED ? j * kStepX : 0);
                     u32x4_t xl[XV];
                     if constexpr (MODE == kF32Group32 && E4M3) {  // k = 32 i + 8 q of instruction i: half a chunk
                         u32x2_t c[4];
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
-                            c[i] = reinterpret_cast<const u32x2_t*>(row + ((2 * i + (q >> 1)) ^ (m & 7)))[q & 1];
+                            c[i] = reinterpret_cast<const u32x2_t*>(
+                                step_x + x_unit(MAXROWS, ROWS, kChunks, m, 2 * i + (q >> 1)))[q & 1];
                         xl[0] = u32x4(c[0].x, c[0].y, c[1].x, c[1].y);
                         xl[1] = u32x4(c[2].x, c[2].y, c[3].x, c[3].y);
                     } else {
 #pragma unroll
                         for (int i = 0; i < XV; ++i)
-                            xl[i] = row[(MODE == kF32Group32 ? 4 * i + q : XV * q + i) ^ (m & (kChunks - 1))];
+                            xl[i] = step_x[x_unit(MAXROWS, ROWS, kChunks, m,
+                                                  MODE == kF32Group32 ? 4 * i + q : XV * q + i)];
                     }
                     const float own = j == 0 ? xs[mt].x : j == 1 ? xs[mt].y : j == 2 ? xs[mt].z : xs[mt].w;
                     multiply(wf, ws, xl, own, acc[mt]);
@@ -565,7 +551,7 @@ __global__ __launch_bounds__(kMaxThreads, 2) void expert_matvec_kernel(MatvecArg
         constexpr int ROWS = decltype(rows_const)::value;
         constexpr int MT = (ROWS + 15) / 16;
         f32x4_t acc[MT][kNT] = {};
-        multiply_rows<E4M3, MODE, ROWS, SHARED, TAIL>(a, sh, m0, lane, wave, mine, x_lds, acc);
+        multiply_rows<E4M3, MODE, MAXROWS, ROWS, SHARED, TAIL>(a, sh, m0, lane, wave, mine, x_lds, acc);
         wave_lds_order();
         float* sums = reinterpret_cast<float*>(mine);
         // the first operand's rows run along a lane's sums, the second's along the lanes
