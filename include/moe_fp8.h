@@ -611,7 +611,7 @@ moe_status moe_balance_loss_backward(const float* grad_loss, const void* logits,
  *                as moe_expand_cast_fp8 and swiglu_cast_fp8 write them.
  *                16-byte aligned.
  * x_sf           fp32 [x_rows, inner / 128] (e4m3), else NULL.
- * row_token      int32 [num_rows], or NULL (then x_rows == num_rows).
+ * row_token      int32 [num_rows], or NULL (then x_rows == num_rows, unless num_rows is 0).
  * num_rows       R >= 0.
  * inner          a multiple of group_size, and of 128 for e4m3 rows.
  * out_width      N >= 1.  inner, N <= MOE_MATVEC_MAX_WIDTH (above:

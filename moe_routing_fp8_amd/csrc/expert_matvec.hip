@@ -665,9 +665,9 @@ extern "C" moe_status moe_expert_matvec(const void* x, int32_t x_dtype, const fl
     if (group_size != 32 && group_size != 128) return MOE_ERR_UNSUPPORTED;
     if (inner % group_size != 0 || (x_dtype == MOE_DTYPE_E4M3 && inner % 128 != 0)) return MOE_ERR_INVALID_ARGUMENT;
     if (expert_offsets == nullptr && num_experts != 1) return MOE_ERR_INVALID_ARGUMENT;
-    if (row_token == nullptr && x_rows != num_rows) return MOE_ERR_INVALID_ARGUMENT;
     if (inner > MOE_MATVEC_MAX_WIDTH || out_width > MOE_MATVEC_MAX_WIDTH) return MOE_ERR_UNSUPPORTED;
-    if (num_rows == 0) return MOE_OK;
+    if (num_rows == 0) return MOE_OK;  // an empty row_token may be null: x_rows is then anything
+    if (row_token == nullptr && x_rows != num_rows) return MOE_ERR_INVALID_ARGUMENT;
     if (w_codes == nullptr || w_sf == nullptr || out_bf16 == nullptr) return MOE_ERR_INVALID_ARGUMENT;
     if (x_rows > 0 && (x == nullptr || (x_dtype == MOE_DTYPE_E4M3) != (x_sf != nullptr)))
         return MOE_ERR_INVALID_ARGUMENT;

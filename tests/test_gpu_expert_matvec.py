@@ -350,3 +350,13 @@ def test_in_a_graph():
         want = go()
         torch.cuda.synchronize()
         assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("x", ["bf16", "e4m3"])
+def test_no_rows_by_token(x):
+    """A batch that reads five rows of x by token and has none of its own."""
+    s = _inputs([0, 0], 8, 128, x, tokens=5)
+    assert s["row_token"].numel() == 0
+    assert _call(s).shape == (0, 8)
+    s.update(expert_offsets=None, w=s["w"][:1], w_sf=s["w_sf"][:1])
+    assert _call(s).shape == (0, 8)

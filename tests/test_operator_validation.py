@@ -122,3 +122,13 @@ def test_expert_matvec(lib):
     assert call(x=FAKE + 8) == INVALID and call(w=FAKE + 8) == INVALID and call(out=FAKE + 1) == INVALID
     assert call(sf=FAKE + 2, ue8m0=0) == INVALID and call(off=FAKE + 2) == INVALID and call(tok=FAKE + 1) == INVALID
     assert call(R=0, X=0, x=None, w=None, sf=None, out=None, off=FAKE) == 0
+
+
+def test_no_rows_by_token(lib):
+    """An empty row_token has no address: no rows, though x has some."""
+    names = ["x", "xd", "xsf", "X", "tok", "R", "K", "N", "E", "off", "w", "sf", "g", "ue8m0", "out", "stream"]
+    call = _caller(lib.moe_expert_matvec, names, [FAKE, 0, None, 5, None, 0, 256, 20, 2, FAKE, FAKE, FAKE, 32, 1, None,
+                                                  None])
+    assert call() == 0 and call(tok=FAKE) == 0
+    assert call(xd=2, xsf=FAKE) == 0
+    assert call(g=16) == UNSUPPORTED and call(K=240) == INVALID and call(off=None) == INVALID
