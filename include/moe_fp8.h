@@ -454,8 +454,8 @@ moe_status swiglu_cast(const uint16_t* gate_up_bf16, int64_t num_rows, int32_t i
  * hidden         H, 1 <= H <= MOE_BLOCK_NORM_MAX_HIDDEN (above:
  *                MOE_ERR_UNSUPPORTED).  Strides >= H.
  * post_weight    fp32 [H], or NULL.
- * gate           fp32 [H] (MOE_GATE_CHANNEL), fp32 [T] (MOE_GATE_TOKEN), NULL
- *                iff gate_mode is MOE_GATE_NONE.
+ * gate           fp32 [H] (MOE_GATE_CHANNEL), fp32 [T] (MOE_GATE_TOKEN; may be
+ *                NULL if T == 0), NULL iff gate_mode is MOE_GATE_NONE.
  * residual_scale any number but NaN.
  * pre_weight     fp32 [H]; given iff normed is.
  * eps            >= 0.

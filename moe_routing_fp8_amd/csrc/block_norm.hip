@@ -428,6 +428,12 @@ bool vec_rows(const void* p, int64_t stride, int32_t dtype) {
     return aligned(p, 16) && stride * dtype_bytes(dtype) % 16 == 0;
 }
 
+// Whether a gate (or its gradient) is there iff its mode asks for one; of no tokens' gate either is right.
+bool gate_given(int mode, const void* gate, int64_t num_tokens) {
+    if (mode == MOE_GATE_TOKEN && num_tokens == 0) return true;
+    return (mode != MOE_GATE_NONE) == (gate != nullptr);
+}
+
 int64_t grad_blocks(int64_t T, int H) {
     const int waves = row_threads(H, 1) / kWave;
     const int64_t most = kComputeUnits * (waves > 8 ? 1 : waves > 4 ? 2 : 4);
@@ -450,7 +456,7 @@ moe_status moe_block_norm(const void* residual, int64_t residual_stride, int32_t
     if (gate_mode != MOE_GATE_NONE && gate_mode != MOE_GATE_CHANNEL && gate_mode != MOE_GATE_TOKEN)
         return MOE_ERR_INVALID_ARGUMENT;
     if (!(eps >= 0.0f) || residual_scale != residual_scale) return MOE_ERR_INVALID_ARGUMENT;
-    if ((gate_mode != MOE_GATE_NONE) != (gate != nullptr)) return MOE_ERR_INVALID_ARGUMENT;
+    if (!gate_given(gate_mode, gate, num_tokens)) return MOE_ERR_INVALID_ARGUMENT;
     if (post_rstd != nullptr && post_weight == nullptr) return MOE_ERR_INVALID_ARGUMENT;
     if (residual_stride < hidden) return MOE_ERR_INVALID_ARGUMENT;
     if (hidden > kMaxHidden || num_tokens > MOE_BLOCK_NORM_MAX_TOKENS) return MOE_ERR_UNSUPPORTED;
@@ -506,7 +512,7 @@ moe_status moe_block_norm_backward(const void* grad_res_out, const void* grad_no
     if (gate_mode != MOE_GATE_NONE && gate_mode != MOE_GATE_CHANNEL && gate_mode != MOE_GATE_TOKEN)
         return MOE_ERR_INVALID_ARGUMENT;
     if (residual_scale != residual_scale) return MOE_ERR_INVALID_ARGUMENT;
-    if ((gate_mode != MOE_GATE_NONE) != (gate != nullptr) || (gate != nullptr) != (grad_gate != nullptr))
+    if (!gate_given(gate_mode, gate, num_tokens) || !gate_given(gate_mode, grad_gate, num_tokens))
         return MOE_ERR_INVALID_ARGUMENT;
     if ((post_weight != nullptr) != (grad_post_weight != nullptr) ||
         (pre_weight != nullptr) != (grad_pre_weight != nullptr))

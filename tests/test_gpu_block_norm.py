@@ -415,3 +415,18 @@ def test_more_than_2_to_31_elements():
     few = moe.moe_block_norm(r[-600:].clone(), y[-600:].clone(), post_weight=w, pre_weight=w)
     assert torch.equal(out[-600:], few[0]) and torch.equal(n[-600:], few[1])
     assert torch.equal(out[:600], moe.moe_block_norm(r[:600], y[:600], post_weight=w, pre_weight=w)[0])
+
+
+@pytest.mark.parametrize("post", [False, True])
+def test_no_tokens_with_a_token_gate(post):
+    H = 96
+    w = torch.ones(H, device="cuda")
+    r, y = torch.empty(0, H, device="cuda"), torch.empty(0, H, dtype=BF16, device="cuda")
+    gate, pw = torch.empty(0, 1, device="cuda"), w if post else None
+    out, normed, post_rstd, pre_rstd = moe.moe_block_norm(r, y, pw, gate, 1.0, w, with_rstd=True)
+    assert out.shape == normed.shape == (0, H) and pre_rstd.shape == (0,)
+    g = {k: torch.full((H,), 7.0, device="cuda") for k in (["grad_post_weight"] if post else []) + ["grad_pre_weight"]}
+    g.update(grad_residual=torch.empty_like(r), grad_y=torch.empty_like(y), grad_gate=torch.empty_like(gate))
+    moe.moe_block_norm_backward(out, normed, out, y, pw, gate, 1.0, w, post_rstd, pre_rstd, out=g)
+    assert int(g["grad_pre_weight"].count_nonzero()) == 0
+    assert not post or int(g["grad_post_weight"].count_nonzero()) == 0

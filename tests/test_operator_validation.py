@@ -132,3 +132,21 @@ def test_no_rows_by_token(lib):
     assert call() == 0 and call(tok=FAKE) == 0
     assert call(xd=2, xsf=FAKE) == 0
     assert call(g=16) == UNSUPPORTED and call(K=240) == INVALID and call(off=None) == INVALID
+
+
+def test_no_tokens_with_a_token_gate(lib):
+    """A gate per token of a batch without tokens has no address."""
+    names = ["r", "rs", "rd", "y", "ys", "ad", "T", "H", "pw", "gate", "mode", "scale", "nw", "eps", "out", "normed",
+             "post", "pre", "stream"]
+    call = _caller(lib.moe_block_norm, names, [None, 64, 0, None, 64, 0, 0, 64, FAKE, None, 2, 1.0, FAKE, 1e-6, None,
+                                               None, None, None, None])
+    assert call() == 0 and call(gate=FAKE) == 0 and call(pw=None) == 0
+    assert call(mode=1) == INVALID and call(mode=0, gate=FAKE) == INVALID and call(T=4) == INVALID
+    names = ["dr", "dn", "out", "outs", "rd", "y", "ys", "ad", "T", "H", "pw", "gate", "mode", "scale", "nw", "post",
+             "pre", "gr", "gy", "gpw", "gg", "gnw", "ws", "wsb", "stream"]
+    call = _caller(lib.moe_block_norm_backward, names,
+                   [None, None, None, 64, 0, None, 64, 0, 0, 64, None, None, 2, 1.0, None, None, None, None, None, None,
+                    None, None, None, 0, None])
+    assert call() == 0 and call(gate=FAKE, gg=FAKE) == 0
+    assert call(mode=1) == INVALID and call(mode=1, gate=FAKE) == INVALID and call(mode=0, gate=FAKE) == INVALID
+    assert call(T=4) == INVALID
