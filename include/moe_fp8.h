@@ -441,7 +441,9 @@ moe_status swiglu_cast(const uint16_t* gate_up_bf16, int64_t num_rows, int32_t i
  *   r' = residual_scale * r + gate * u              (gate NULL: 1)
  *   n  = r' * rsqrt(mean(r'^2) + eps) * pre_weight
  * in fp32; r' and n are rounded once each (to nearest even), n from the
- * unrounded r'.  The sum of a row's squares must stay finite in fp32.
+ * unrounded r'.  The sum of a row's squares must stay finite in fp32; with
+ * eps == 0, a mean of squares below 2^-126 has the precision of fp32's
+ * subnormal numbers, and one that rounds to 0 gives a factor of infinity.
  *   y NULL        no block: r' = r and only n is computed (then post_weight,
  *                 gate and res_out must be NULL and residual_scale 1).
  *   normed NULL   no norm before the next block (then pre_weight and pre_rstd

@@ -37,12 +37,17 @@ constexpr int kMaxHidden = MOE_BLOCK_NORM_MAX_HIDDEN;
 constexpr int64_t kComputeUnits = 256;
 
 // 1 / sqrt(v): the hardware's estimate and one Newton step, which brings it
-// to within 1 ulp (0 and infinity keep the estimate's value).
+// to within 1 ulp (0 and infinity keep the estimate's value).  The estimate
+// takes a subnormal v, which eps = 0 lets through, for 0: v is scaled by 2^24
+// there, and the root by 2^12.
 __device__ __forceinline__ float rsqrt_f32(float v) {
-    const float r = __builtin_amdgcn_rsqf(v);
-    const float e = __builtin_fmaf(-v * r, r, 1.0f);
-    const float n = __builtin_fmaf(0.5f * r, e, r);
-    return v > 0.0f && v < INFINITY ? n : r;
+    const bool tiny = v < 0x1p-126f;
+    const float s = tiny ? v * 0x1p24f : v;
+    const float r = __builtin_amdgcn_rsqf(s);
+    const float e = __builtin_fmaf(-s * r, r, 1.0f);
+    float n = __builtin_fmaf(0.5f * r, e, r);
+    n = s > 0.0f && s < INFINITY ? n : r;
+    return tiny ? n * 0x1p12f : n;
 }
 
 // Rows of more bytes than this in all are read and written past the caches

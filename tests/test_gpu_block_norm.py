@@ -430,3 +430,25 @@ def test_no_tokens_with_a_token_gate(post):
     moe.moe_block_norm_backward(out, normed, out, y, pw, gate, 1.0, w, post_rstd, pre_rstd, out=g)
     assert int(g["grad_pre_weight"].count_nonzero()) == 0
     assert not post or int(g["grad_post_weight"].count_nonzero()) == 0
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("H", [64, 2049, 9001])
+@pytest.mark.parametrize("size", [1e-18, 1e-19, 3e-20, 1e-20, 1e-21])
+def test_tiny_rows_without_eps(dtype, H, size):
+    """eps = 0 and mean squares around and below fp32's smallest normal value.  A square, and the mean, are then off
+    by up to half a step of 2^-149 each: the mean by 2^-149, the factor by half of that share of it."""
+    g = torch.Generator().manual_seed(H)
+    v = (size * (1 + torch.rand(3, H, generator=g))).to(dtype)
+    one = torch.ones(H)
+    _, n, _, pre = moe.moe_block_norm(v.cuda(), pre_weight=one.cuda(), eps=0.0, with_rstd=True)
+    r, _, post, _ = moe.moe_block_norm(torch.zeros(3, H, device="cuda"), v.cuda(), post_weight=one.cuda(), eps=0.0,
+                                       with_rstd=True)
+    mean = v.double().square().mean(1)
+    want = mean.rsqrt()
+    share = ROUNDINGS * EPS32 + 2.0 ** -149 / mean
+    for rstd in (pre, post):
+        _close(rstd, want, share * want, "rstd")
+    want = v.double() * want[:, None]
+    _close(n, want, share[:, None] * want.abs(), "normed")
+    _close(r, want, share[:, None] * want.abs(), "res_out")
