@@ -211,7 +211,7 @@ __device__ __forceinline__ float row_scores(const float (&z)[S::P], float (&w)[S
         const bool low = m < -60.0f;
 #pragma unroll
         for (int j = 0; j < S::P; ++j) {
-            const float t = exp_nonpos(-fabsf(z[j]));
+            const float t = exp_nonpos_exact(-fabsf(z[j]));
             const float r = rcp_f32(1.0f + t);
             w[j] = z[j] > 0.0f ? r : t * r;
             comp[j] = z[j] > 0.0f ? t * r : r;

@@ -64,11 +64,23 @@ __device__ __forceinline__ int wave_sum_i32(int x) {
     return static_cast<int>(halves[0] + halves[1]);
 }
 
-// exp(x) for x <= 0 (and NaN) by the hardware exp2: the rounded product x *
-// log2(e) costs a relative error of |x| * 2^-24 (about 1e-6 at x = -16, where
-// the value is 1e-7), which the scores' normalisation carries over unchanged.
+// exp(x) for x <= 0 (and NaN) by the hardware exp2.  The rounded product x *
+// log2(e) costs a relative error of |x| * 2^-24: for an x that is a difference
+// of fp32 values, as large as these are the softmax's, whose rounding costs as
+// much.
 __device__ __forceinline__ float exp_nonpos(float x) {
     return __builtin_amdgcn_exp2f(x * 1.44269504088896340736f);
+}
+
+// The same to 1.5 ulp, for an exact x: with h the rounded product, exp(x) =
+// exp2(h) * exp(x - h ln 2), the second factor within 2^-17 of 1.  (Below -128
+// both are 0.)
+__device__ __forceinline__ float exp_nonpos_exact(float x) {
+    constexpr float kLn2 = 0.693147180559945309417f, kLn2Low = static_cast<float>(0.693147180559945309417 - kLn2);
+    x = x < -128.0f ? -128.0f : x;
+    const float h = x * 1.44269504088896340736f;
+    const float e = __builtin_amdgcn_exp2f(h);
+    return __builtin_fmaf(e, __builtin_fmaf(-h, kLn2Low, __builtin_fmaf(-h, kLn2, x)), e);
 }
 
 // bf16 bit pattern (round to nearest even) of an fp32 value, and two packed.

@@ -371,3 +371,22 @@ def test_more_than_2_to_31_elements():
     assert torch.equal(o["counts"][0], torch.bincount(ids[:-50].flatten(), minlength=E).int())
     assert abs(float(o["loss"][1] - few["loss"][0])) <= 1e-5 * float(few["loss"][0])  # other order of 50 additions
     assert torch.equal(grad[-50:], alone)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("center", [-59.0, -40.0, -20.0, -4.0, 4.0])
+def test_sigmoid_scores_of_low_rows(dtype, center):
+    """One token's p.  A score takes an exponential (1 ulp and half of one), 1 + t, its reciprocal (1 ulp) and a
+    product: at most 7 roundings of 2^-24, 7 / sqrt(3) in the mean square over the experts.  What all of a row share is
+    the sum's error: some 20 additions, whose roundings meet at random (20 ** 0.5 / sqrt(3)), and four factors.  All
+    of it stays below 8 roundings in the mean square; the argument's size must not enter."""
+    E = 256
+    g = torch.Generator().manual_seed(7)
+    z = (center + 0.5 * torch.randn(8, E, generator=g)).to(dtype)
+    assert float(z.max(1).values.min()) > -60
+    off = torch.arange(9, dtype=torch.int32)
+    o = moe.moe_balance_loss(z.cuda(), z.float().topk(4, 1).indices.cuda(), score="sigmoid", seq_offsets=off.cuda())
+    want = _probs64(z.double(), "sigmoid")
+    err = (o["prob_mean"].double().cpu() / want - 1).square().mean(1).sqrt()
+    _log(f"sigmoid near {center} {dtype}: {float(err.max()) / EPS32:.2f} roundings")
+    assert float(err.max()) <= 8 * EPS32
