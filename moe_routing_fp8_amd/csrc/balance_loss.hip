@@ -577,8 +577,11 @@ __global__ __launch_bounds__(kGradThreads) void balance_grad_kernel(
 }
 
 // Calls f.template operator()<TL, S, V, SIGMOID>() for the row shape.  V: 16
-// bytes of logits where every row starts on such a boundary (gradients and
-// counts as well) and E fills whole vectors, else single values.
+// bytes of logits (8 where a lane holds four bf16 values) where every row
+// starts on a 16-byte boundary (gradients and counts as well) and E fills
+// whole vectors, else single values.  131072 x 64 bf16, forward and backward:
+// 18.8 and 13.4 us, with single values 23.0 and 15.6; 131072 x 24 fp32: 17.6
+// and 12.5 against 19.1 and 12.8.  Up to 16 experts a lane holds one value.
 template <typename TL, typename S, typename F>
 hipError_t with_vec(bool vec, int score, F&& f) {
     constexpr int V = S::P * TL::kBytes < 16 ? S::P : 16 / TL::kBytes;
@@ -591,10 +594,10 @@ hipError_t with_vec(bool vec, int score, F&& f) {
 template <typename TL, typename F>
 hipError_t with_row(const void* logits, const void* grad, const void* counts, int64_t stride, int E, int score,
                     F&& f) {
-    const bool vec = E >= 64 && E % (16 / TL::kBytes) == 0 && aligned(logits, 16) && aligned(grad, 16) &&
+    const bool vec = E % (16 / TL::kBytes) == 0 && aligned(logits, 16) && aligned(grad, 16) &&
                      aligned(counts, 16) && stride * TL::kBytes % 16 == 0;
     if (E <= 16) return with_vec<TL, RowShape<16, 1>>(false, score, f);
-    if (E <= 64) return with_vec<TL, RowShape<16, 4>>(vec && TL::kBytes == 4, score, f);
+    if (E <= 64) return with_vec<TL, RowShape<16, 4>>(vec, score, f);
     if (E <= 128) return with_vec<TL, RowShape<16, 8>>(vec, score, f);
     if (E <= kNarrowExperts) return with_vec<TL, RowShape<16, 16>>(vec, score, f);
     if (E <= 512) return with_vec<TL, RowShape<64, 8>>(vec, score, f);

@@ -107,9 +107,6 @@ struct Bf16 {
         } else if constexpr (VEC == 4) {
             const uint2 r = *reinterpret_cast<const uint2*>(q);
             f[0] = bf16_lo(r.x); f[1] = bf16_hi(r.x); f[2] = bf16_lo(r.y); f[3] = bf16_hi(r.y);
-        } else if constexpr (VEC == 2) {
-            const uint32_t r = *reinterpret_cast<const uint32_t*>(q);
-            f[0] = bf16_lo(r); f[1] = bf16_hi(r);
         } else {
             static_assert(VEC == 1, "vector width");
             f[0] = __uint_as_float(static_cast<uint32_t>(*q) << 16);
@@ -127,8 +124,6 @@ struct Bf16 {
             }
         } else if constexpr (VEC == 4) {
             *reinterpret_cast<uint2*>(q) = make_uint2(bf16_pack2(f[0], f[1]), bf16_pack2(f[2], f[3]));
-        } else if constexpr (VEC == 2) {
-            *reinterpret_cast<uint32_t*>(q) = bf16_pack2(f[0], f[1]);
         } else {
             static_assert(VEC == 1, "vector width");
             *q = bf16_bits(f[0]);
@@ -148,9 +143,6 @@ struct F32 {
                 f[4 * v] = __uint_as_float(r.x); f[4 * v + 1] = __uint_as_float(r.y);
                 f[4 * v + 2] = __uint_as_float(r.z); f[4 * v + 3] = __uint_as_float(r.w);
             }
-        } else if constexpr (VEC == 2) {
-            const float2 r = *reinterpret_cast<const float2*>(q);
-            f[0] = r.x; f[1] = r.y;
         } else {
             static_assert(VEC == 1, "vector width");
             f[0] = *q;
@@ -163,8 +155,6 @@ struct F32 {
 #pragma unroll
             for (int v = 0; v < VEC / 4; ++v)
                 reinterpret_cast<float4*>(q)[v] = make_float4(f[4 * v], f[4 * v + 1], f[4 * v + 2], f[4 * v + 3]);
-        } else if constexpr (VEC == 2) {
-            *reinterpret_cast<float2*>(q) = make_float2(f[0], f[1]);
         } else {
             static_assert(VEC == 1, "vector width");
             *q = f[0];

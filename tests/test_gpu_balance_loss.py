@@ -390,3 +390,13 @@ def test_sigmoid_scores_of_low_rows(dtype, center):
     err = (o["prob_mean"].double().cpu() / want - 1).square().mean(1).sqrt()
     _log(f"sigmoid near {center} {dtype}: {float(err.max()) / EPS32:.2f} roundings")
     assert float(err.max()) <= 8 * EPS32
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("E", [17, 20, 24, 32, 40, 48, 63, 64])
+def test_rows_of_few_experts(E, dtype, score):
+    """Whole vectors of logits and single values, a row's vectors on some of its lanes."""
+    s = _inputs(300, E, 4, dtype, cuts=[0, 130, 131, 290], masked=0.1, seed=E)
+    o, g = _run(_gpu(s), score)
+    _check(s, o, g, score)
