@@ -400,3 +400,23 @@ def test_rows_of_few_experts(E, dtype, score):
     s = _inputs(300, E, 4, dtype, cuts=[0, 130, 131, 290], masked=0.1, seed=E)
     o, g = _run(_gpu(s), score)
     _check(s, o, g, score)
+
+
+@pytest.mark.parametrize("T,E,short", [(33000, 64, 16), (33000, 64, 60), (9000, 1024, 20), (5000, 256, 300)])
+def test_a_long_sequence_beside_short_ones(T, E, short):
+    """One sequence with most of the chunks' slots, and short ones before and after it."""
+    _log(f"T={T} E={E} short={short}")
+    half = short // 2
+    cuts = list(range(0, 3 * half + 1, 3)) + list(range(T - 5 * (short - half), T + 1, 5))
+    s = _inputs(T, E, 4, F32, cuts=cuts, masked=0.05, seed=short)
+    assert s["grad_loss"].numel() == short + 1
+    o, g = _run(_gpu(s), "softmax")
+    _check(s, o, g, "softmax")
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_many_rows_of_1024_experts(dtype):
+    """The most LDS that a workgroup takes."""
+    s = _inputs(4200, 1024, 8, dtype, seed=12)
+    o, g = _run(_gpu(s), "sigmoid")
+    _check(s, o, g, "sigmoid")
