@@ -624,7 +624,9 @@ moe_status moe_balance_loss_backward(const float* grad_loss, const void* logits,
  * w_codes        e2m1 [E, N, inner / 2] bytes, code 2i in the low nibble of
  *                byte i, 16-byte aligned.
  * w_sf           [E, N, inner / group_size]: UE8M0 bytes (sf_ue8m0 = 1) or
- *                fp32 (0).
+ *                fp32 (0).  A byte b stands for 2^(b - 127) and 255 for NaN;
+ *                every code times it is exact, also where it is subnormal,
+ *                and infinite from 2^128 on (b = 253 and 254 only).
  * group_size     32 or 128 (anything else: MOE_ERR_UNSUPPORTED).
  * out_bf16       bf16 [R, N] output.
  */

@@ -360,3 +360,28 @@ def test_no_rows_by_token(x):
     assert _call(s).shape == (0, 8)
     s.update(expert_offsets=None, w=s["w"][:1], w_sf=s["w_sf"][:1])
     assert _call(s).shape == (0, 8)
+
+
+@pytest.mark.parametrize("K", [512, 32])
+def test_scale_bytes_at_the_ends(K):
+    """Each code under the scale bytes whose products leave bf16's normal range, and under 255, by rows of weights with
+    one code that is not zero; K = 32 takes the code for the last steps."""
+    bytes_ = [0, 1, 2, 3, 126, 127, 252, 253, 254, 255]
+    N = 16 * len(bytes_)
+    w = torch.zeros(1, N, K // 2, dtype=torch.uint8)
+    at = (torch.arange(N) * 13) % K
+    code = torch.arange(N) % 16
+    w[0, torch.arange(N), at // 2] = (code << (4 * (at % 2))).to(torch.uint8)
+    sf = torch.full((1, N, K // 32), 127, dtype=torch.uint8)
+    b = torch.tensor(bytes_, dtype=torch.uint8).repeat_interleave(16)
+    sf[0, torch.arange(N), at // 32] = b
+    for x in (1.0, -1.0, 2.0 ** -20, 2.0 ** 20):
+        s = {"x": torch.full((3, K), x, dtype=torch.bfloat16), "x_sf": None, "row_token": None, "w": w, "w_sf": sf,
+             "expert_offsets": None}
+        got = _call(s).float().cpu()
+        weight = VALUES[code] * torch.pow(2.0, b.double() - 127)
+        weight = torch.where(weight.abs() >= 2.0 ** 128, weight.sign() * float("inf"), weight)
+        want = (weight * x).float().to(torch.bfloat16).float()
+        nan = b == 255
+        assert torch.isnan(got[:, nan]).all()
+        assert torch.equal(got[:, ~nan], want[~nan].expand(3, -1)), x
