@@ -556,8 +556,8 @@ size_t moe_balance_loss_workspace_bytes(int64_t num_tokens, int32_t num_experts,
  * topk_idx       int64 [T, K] (from moe_topk_gate or any source); an id
  *                outside [0, E) is not counted.
  * num_topk       K, 1 <= K <= min(E, 16).
- * token_mask     uint8 [T], 0 = not live (the token's logits and ids are not
- *                read), or NULL.
+ * token_mask     uint8 [T], 0 = not live (the token's logits and ids may hold
+ *                anything; their memory is still read), or NULL.
  * seq_offsets    int32 [S + 1], non-decreasing, within [0, T]: sequence s is
  *                the tokens [seq_offsets[s], seq_offsets[s + 1]); tokens
  *                outside all of them belong to none.  NULL: one sequence of
