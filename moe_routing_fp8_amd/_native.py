@@ -850,8 +850,8 @@ def moe_block_norm(residual: torch.Tensor, y: Optional[torch.Tensor] = None,
         with _alloc_on(stream):
             out = (torch.empty((T, H), dtype=residual.dtype, device=dev) if y is not None else None,
                    torch.empty((T, H), dtype=act_dtype, device=dev) if pre_weight is not None else None,
-                   torch.empty(T, device=dev) if with_rstd and post_weight is not None else None,
-                   torch.empty(T, device=dev) if with_rstd and pre_weight is not None else None)
+                   torch.empty(T, dtype=torch.float32, device=dev) if with_rstd and post_weight is not None else None,
+                   torch.empty(T, dtype=torch.float32, device=dev) if with_rstd and pre_weight is not None else None)
         res_out, normed, post_rstd, pre_rstd = out
     else:
         res_out, normed, post_rstd, pre_rstd = out
@@ -911,11 +911,12 @@ def moe_block_norm_backward(grad_res_out: Optional[torch.Tensor], grad_normed: O
         raise ValueError("moe_block_norm_backward: without y there is only the norm before the next block")
     if out is None:
         with _alloc_on(stream):
+            f32 = {"dtype": torch.float32, "device": dev}
             out = {"grad_residual": torch.empty((T, H), dtype=res_out.dtype, device=dev),
                    "grad_y": torch.empty((T, H), dtype=act_dtype, device=dev) if y is not None else None,
-                   "grad_post_weight": torch.empty(H, device=dev) if post_weight is not None else None,
-                   "grad_gate": torch.empty(gate.shape, device=dev) if gate is not None else None,
-                   "grad_pre_weight": torch.empty(H, device=dev) if pre_weight is not None else None}
+                   "grad_post_weight": torch.empty(H, **f32) if post_weight is not None else None,
+                   "grad_gate": torch.empty(gate.shape, **f32) if gate is not None else None,
+                   "grad_pre_weight": torch.empty(H, **f32) if pre_weight is not None else None}
     else:
         for key, dtype, shape, src in (("grad_residual", res_out.dtype, (T, H), res_out),
                                        ("grad_y", act_dtype, (T, H), y),
@@ -981,9 +982,10 @@ def moe_balance_loss(logits: torch.Tensor, topk_idx: torch.Tensor, score: str = 
     _need_out(topk_idx, torch.int64, (T, K), "topk_idx", dev)
     if out is None:
         with _alloc_on(stream):
-            out = {"loss": torch.empty(S, device=dev), "counts": torch.empty((S, E), dtype=torch.int32, device=dev),
+            out = {"loss": torch.empty(S, dtype=torch.float32, device=dev),
+                   "counts": torch.empty((S, E), dtype=torch.int32, device=dev),
                    "seq_tokens": torch.empty(S, dtype=torch.int32, device=dev),
-                   "prob_mean": torch.empty((S, E), device=dev)}
+                   "prob_mean": torch.empty((S, E), dtype=torch.float32, device=dev)}
     else:
         for key, dtype, shape in (("loss", torch.float32, (S,)), ("counts", torch.int32, (S, E)),
                                   ("seq_tokens", torch.int32, (S,)), ("prob_mean", torch.float32, (S, E))):

@@ -420,3 +420,16 @@ def test_many_rows_of_1024_experts(dtype):
     s = _inputs(4200, 1024, 8, dtype, seed=12)
     o, g = _run(_gpu(s), "sigmoid")
     _check(s, o, g, "sigmoid")
+
+
+def test_outputs_under_another_default_type():
+    """torch's default type has no say in the loss's and the means' type."""
+    d = _gpu(_inputs(500, 64, 4, cuts=[0, 200, 500]))
+    want, gwant = _run(d, "softmax")
+    torch.set_default_dtype(BF16)
+    try:
+        got, grad = _run(d, "softmax")
+    finally:
+        torch.set_default_dtype(F32)
+    assert all(got[k].dtype == want[k].dtype and torch.equal(got[k], want[k]) for k in want)
+    assert torch.equal(grad, gwant)

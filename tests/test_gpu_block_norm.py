@@ -452,3 +452,18 @@ def test_tiny_rows_without_eps(dtype, H, size):
     want = v.double() * want[:, None]
     _close(n, want, share[:, None] * want.abs(), "normed")
     _close(r, want, share[:, None] * want.abs(), "res_out")
+
+
+def test_outputs_under_another_default_type():
+    """torch's default type has no say in the rstds' and the parameter gradients' type."""
+    d = _gpu(_inputs(40, 520, F32, BF16))
+    want = _forward(d)
+    gwant = _backward(d, want[0], want[2], want[3])
+    torch.set_default_dtype(BF16)
+    try:
+        got = _forward(d)
+        grads = _backward(d, got[0], got[2], got[3])
+    finally:
+        torch.set_default_dtype(F32)
+    for a, b in [*zip(got, want), *((grads[k], gwant[k]) for k in gwant)]:
+        assert a.dtype == b.dtype and torch.equal(a, b)
