@@ -824,7 +824,7 @@ def moe_block_norm(residual: torch.Tensor, y: Optional[torch.Tensor] = None,
     gate fp32 [H] or [T, 1].  Returns (r', n, post_rstd, pre_rstd): r' in the residual's type (None without y), n in
     y's (`act_dtype`, by default the residual's, without y; None without pre_weight), and with `with_rstd` the
     fp32 [T] factors that the backward pass reads (else None).  `out`: these four; r' may be the residual
-    itself."""
+    itself.  Nothing is recorded for autograd: the gradients come from moe_block_norm_backward."""
     rs = _need_rows(residual, "residual")
     T, H = residual.shape
     dev = residual.device
@@ -972,7 +972,8 @@ def moe_balance_loss(logits: torch.Tensor, topk_idx: torch.Tensor, score: str = 
     """The balance loss of each packed sequence: logits bf16 or fp32 [T, E] (any row stride), topk_idx int64 [T, K],
     token_mask bool [T] (False: not live), seq_offsets int32 [S+1] (None: one sequence) -> dict of loss fp32 [S],
     counts int32 [S, E], seq_tokens int32 [S] (live tokens) and prob_mean fp32 [S, E].  `score`: "softmax", or
-    "sigmoid" divided by the row's sum."""
+    "sigmoid" divided by the row's sum.  Nothing is recorded for autograd: the gradient comes from
+    moe_balance_loss_backward."""
     stride, mode, S = _balance_inputs(logits, score, token_mask, seq_offsets)
     T, E = logits.shape
     if topk_idx.dim() != 2:
