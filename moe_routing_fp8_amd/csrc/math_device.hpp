@@ -72,15 +72,15 @@ __device__ __forceinline__ float exp_nonpos(float x) {
     return __builtin_amdgcn_exp2f(x * 1.44269504088896340736f);
 }
 
-// The same to 1.5 ulp, for an exact x: with h the rounded product, exp(x) =
-// exp2(h) * exp(x - h ln 2), the second factor within 2^-17 of 1.  (Below -128
-// both are 0.)
+// The same for an exact x, to 1.5 ulp and |x| * 2^-28: with h the rounded
+// product, exp(x) = exp2(h) * exp(x - h ln 2), where the second argument is
+// below 2^-16 as long as the result is not 0.  Its clamp, which a NaN leaves
+// as -1, is for x so low that the difference means nothing, -inf among them.
+// (The second difference's own constant leaves the |x| * 2^-28.)
 __device__ __forceinline__ float exp_nonpos_exact(float x) {
-    constexpr float kLn2 = 0.693147180559945309417f, kLn2Low = static_cast<float>(0.693147180559945309417 - kLn2);
-    x = x < -128.0f ? -128.0f : x;
     const float h = x * 1.44269504088896340736f;
     const float e = __builtin_amdgcn_exp2f(h);
-    return __builtin_fmaf(e, __builtin_fmaf(-h, kLn2Low, __builtin_fmaf(-h, kLn2, x)), e);
+    return __builtin_fmaf(e, __builtin_amdgcn_fmed3f(__builtin_fmaf(-h, 0.693147180559945309417f, x), -1.0f, 1.0f), e);
 }
 
 // bf16 bit pattern (round to nearest even) of an fp32 value, and two packed.
