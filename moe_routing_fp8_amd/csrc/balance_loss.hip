@@ -23,11 +23,14 @@
 // batch of one chunk takes its losses in the first launch.
 // No floating atomics: the results do not depend on timing.
 //
-// Kernel traces (sums, slots, [loss], gradient), beside a launch of nothing at 3.8 us:
-//   32768 x 256 fp32, one sequence      10.9 + 4.8 + 2.4 + 12.3 us; the sums read 3.3 TB/s: as many
+// Kernel traces (sums, slots, [loss], gradient); a kernel that does nothing takes 1.3 us there:
+//   32768 x 256 fp32, one sequence      11.5 + 4.8 + 2.4 + 12.4 us; the sums read 2.9 to 3.3 TB/s: as many
 //                                       steps of the row reductions and exponentials as loads
-//   4096 x 256 bf16, eight sequences    7.9 + 5.5 + 5.4 us, latency
-//   10007 x 61 fp32, 311 sequences      9.0 + 3.8 + 5.8 us, latency
+//   the same with sigmoid scores        14.6 + 4.8 + 2.4 + 15.6 us
+//   the same in 20 sequences, one of    17.0 + 26.5 + 11.8 us: one workgroup adds the long one's thousand slots
+//   30000 tokens
+//   4096 x 256 bf16, eight sequences    8.8 + 5.2 + 5.4 us, latency (sigmoid scores)
+//   10007 x 61 fp32, 311 sequences      9.2 + 4.1 + 5.8 us, latency
 //   64 x 16 fp32, one sequence          4.4 us in one launch, latency
 // Backward, one launch: the same lanes per token read the row again, with the
 // sequence's counts in registers.
@@ -69,7 +72,8 @@ constexpr int kManySeqs = 4;
 constexpr int64_t kOneLaunchSteps = 4;
 constexpr int kOneLaunchSeqs = 8;
 // Up to this many slots per sequence, on average, one workgroup adds all of a sequence's; above, its columns are
-// split over workgroups and the loss takes a launch of its own.
+// split over workgroups and the loss takes a launch of its own.  The offsets are on the device, so the average is
+// all that the host knows: one sequence that has most of the slots of 20 takes 26 us here.
 constexpr int64_t kOneLevelSlots = 64;
 constexpr int kReduceCols = 16;  // columns of a workgroup of the split sum: 64-byte pieces of each slot
 
@@ -621,8 +625,8 @@ struct SumsLauncher {
     hipError_t operator()() const {
         const size_t lds = (static_cast<size_t>(plan.waves + 1) * E + 1 + plan.waves) * sizeof(float);
         hipLaunchKernelGGL((balance_sums_kernel<TL, S, V, SIGMOID>), dim3(static_cast<unsigned>(plan.num_chunks)),
-                           dim3(plan.waves * kWave), lds, stream, logits, stride, E, topk_idx, K, mask, seqs, plan.chunk,
-                           sums, counts, tokens, out);
+                           dim3(plan.waves * kWave), lds, stream, logits, stride, E, topk_idx, K, mask, seqs,
+                           plan.chunk, sums, counts, tokens, out);
         return hipGetLastError();
     }
 };

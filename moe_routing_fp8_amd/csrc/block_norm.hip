@@ -15,12 +15,18 @@
 // running sums in registers, and writes them once; a second launch adds the
 // workgroups' sums in order.
 //
-// Bound by the bytes of the rows; kernel traces:
-//   forward, 4096 x 7168, bf16                     48.5 us  4.8 TB/s
-//   backward, 4096 x 7168, fp32 r and bf16 y       104.8 + 5.4 us  4.8 TB/s
-//   backward, 1021 x 2049, bf16 (cached)           16.4 + 3.9 us: the three dependent sums of two rows in turn
-//   forward, one row of 7168, bf16                 3.9 us: a launch and the two dependent sums
-// A large copy runs at 5.2 TB/s.
+// Kernel traces (a kernel that does nothing: 1.3 us; a large copy runs at 5.2
+// TB/s).  Bound by the bytes of the rows:
+//   forward, 4096 x 7168, bf16                     48.6 us  4.8 TB/s
+//   forward, no norm after the block and no gate   41.7 us  5.6 TB/s
+//   backward, 4096 x 7168, fp32 r and bf16 y       105.2 + 5.4 us  4.8 TB/s
+//   backward, 4096 x 7168, fp32                    146.3 + 5.4 us  4.6 TB/s, with 12 registers spilled
+// and by the latency of a row's dependent sums:
+//   forward, one row of 7168, bf16                 4.0 us
+//   backward, 4096 x 7168, bf16                    87.5 + 5.3 us  3.8 TB/s
+//   backward, 1021 x 2049, bf16 (cached)           16.4 + 4.0 us, two rows in turn; its bytes take 4.9
+//   backward, 16384 x 256, bf16 (cached)           30.7 + 4.7 us, 16 rows in turn; its bytes take 9.8
+//   backward, 2048 x 16384, bf16                   250.7 + 9.0 us, with 80 registers spilled
 #include <hip/hip_runtime.h>
 
 #include "api_common.hpp"
@@ -32,8 +38,10 @@ namespace {
 
 constexpr int kMaxRowThreads = 1024;
 constexpr int kMaxHidden = MOE_BLOCK_NORM_MAX_HIDDEN;
-// Workgroups of the backward pass: as many as keep 16 waves on each of the 256
-// compute units, one to four; each leaves one row of partial sums.
+// The backward pass takes one workgroup for each compute unit, two up to
+// eight waves a row and four up to four, no more than 16 waves a compute unit
+// (a single one for rows of one wave gives it four); each leaves one row of
+// partial sums.
 constexpr int64_t kComputeUnits = 256;
 
 // 1 / sqrt(v): the hardware's estimate and one Newton step, which brings it
@@ -197,6 +205,9 @@ struct GradRow {
 // hidden 7168, so nothing else would cover a row's loads; reading the three
 // parameters again for each row would add 86 KB from the caches to the 129 KB
 // of the row.  Without (rows of more than 8 values a thread): neither fits.
+// A workgroup of up to 1024 threads leaves a thread 128 registers: that holds
+// one vector of a row unless both streams are fp32 (12 to 25 spilled), and two
+// vectors not at all (78 to 702 spilled).
 // AS: of the loads; OUT: of the stores.
 template <typename TR, typename TA, int VPT, Access AS, Access OUT>
 __global__ __launch_bounds__(kMaxRowThreads) void block_norm_grad_kernel(NormGradArgs a) {

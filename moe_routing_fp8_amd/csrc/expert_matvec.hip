@@ -11,13 +11,19 @@
 //
 // Measured, from kernel traces (weights, scales, rows and results over the time):
 //   one token's 8 experts, 7168 -> 4096, UE8M0 scales, bf16 x   25 us    5.0 TB/s
-//   128 rows, 32 experts, 7168 -> 4096, UE8M0 scales, e4m3 x    80 to 88 us, 5.6 to 6.1 TB/s
-//   512 rows, 32 experts, 2048 -> 7168, fp32 scales, bf16 x     62 to 65 us, 4.0 to 4.2 TB/s
-//   one row, one expert, 2048 -> 7168, UE8M0 scales, bf16 x     5.1 us   (latency: a launch and two blocks of k)
-// A bare streaming read of such arrays reaches 6.1 to 7.0 TB/s.  With few rows
+//   128 rows, 32 experts, 7168 -> 4096, UE8M0 scales, e4m3 x    79 to 89 us, 5.5 to 6.2 TB/s
+//   128 rows, 32 experts, 7168 -> 4096, fp32 scales of 32       115 to 123 us, 4.7 to 5.0 TB/s
+//   512 rows, 32 experts, 2048 -> 7168, fp32 scales, bf16 x     60 to 65 us, 4.0 to 4.3 TB/s
+//   one token's 4 experts, 2880 -> 5760, UE8M0 scales, bf16 x   20 us    1.7 TB/s (k ends inside a block)
+//   one row, one expert, 2048 -> 7168, UE8M0 scales, bf16 x     5.1 us   (latency: loads, one block of k, the join of
+//                                                               four waves' shares; an empty kernel takes 1.3)
+// A bare streaming read of such arrays reaches 6.6 to 7.0 TB/s.  With few rows
 // the start and the drain of a launch of one round of waves bound it; with 16
 // and more rows the registers, which allow two waves a SIMD and so bound the
-// loads in flight while the matrix cores and the conversions work.
+// loads in flight while the matrix cores and the conversions work.  They do
+// not hold everything everywhere: 2 to 10 are spilled in passes of 32 rows
+// (the 512 rows above), 2 to 10 in passes of 16 with fp32 scales of 32, and
+// 24 to 48 in those where k ends inside a block.
 //
 // Products.  An e2m1 value is exact in bf16, and so is an e4m3 value of x, so
 // both go through the bf16 matrix instruction with exact products and fp32
