@@ -822,9 +822,9 @@ def moe_block_norm(residual: torch.Tensor, y: Optional[torch.Tensor] = None,
     u = rmsnorm(y) * post_weight, r' = residual_scale * residual + gate * u, n = rmsnorm(r') * pre_weight.
     residual [T, H] and y [T, H] (None: no block, r' = residual) are bf16 or fp32, each with any row stride;
     gate fp32 [H] or [T, 1].  Returns (r', n, post_rstd, pre_rstd): r' in the residual's type (None without y), n in
-    y's (`act_dtype`, by default the residual's, without y; None without pre_weight), and with `with_rstd` the
-    fp32 [T] factors that the backward pass reads (else None).  `out`: these four; r' may be the residual
-    itself.  Nothing is recorded for autograd: the gradients come from moe_block_norm_backward."""
+    y's (without y `act_dtype`, by default that of `out`'s n or else the residual's; None without pre_weight), and
+    with `with_rstd` the fp32 [T] factors that the backward pass reads (else None).  `out`: these four; r' may be the
+    residual itself.  Nothing is recorded for autograd: the gradients come from moe_block_norm_backward."""
     rs = _need_rows(residual, "residual")
     T, H = residual.shape
     dev = residual.device
@@ -838,7 +838,7 @@ def moe_block_norm(residual: torch.Tensor, y: Optional[torch.Tensor] = None,
             raise ValueError(f"act_dtype {act_dtype}: y is {y.dtype}")
         act_dtype = y.dtype
     elif act_dtype is None:
-        act_dtype = residual.dtype
+        act_dtype = residual.dtype if out is None or out[1] is None else out[1].dtype
     if act_dtype not in _NORM_DTYPES:
         raise ValueError(f"act_dtype: expected bf16 or fp32, got {act_dtype}")
     _need_param(post_weight, H, "post_weight", dev)

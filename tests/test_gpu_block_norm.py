@@ -467,3 +467,18 @@ def test_outputs_under_another_default_type():
         torch.set_default_dtype(F32)
     for a, b in [*zip(got, want), *((grads[k], gwant[k]) for k in gwant)]:
         assert a.dtype == b.dtype and torch.equal(a, b)
+
+
+@pytest.mark.parametrize("res,act", TYPES)
+def test_the_norm_alone_takes_its_type_from_the_output(res, act):
+    """Without y, and without act_dtype, a given n says which type it is to have."""
+    d = _gpu(_inputs(6, 200, res, act, block=False))
+    want = moe.moe_block_norm(d["residual"], pre_weight=d["pre_weight"], act_dtype=act, with_rstd=True)
+    n, rstd = torch.empty(6, 200, dtype=act, device="cuda"), torch.empty(6, device="cuda")
+    got = moe.moe_block_norm(d["residual"], pre_weight=d["pre_weight"], out=(None, n, None, rstd))
+    assert got[1] is n and torch.equal(n, want[1]) and torch.equal(rstd, want[3])
+    other = BF16 if act == F32 else F32
+    with pytest.raises(ValueError, match="normed"):
+        moe.moe_block_norm(d["residual"], pre_weight=d["pre_weight"], act_dtype=other, out=(None, n, None, rstd))
+    with pytest.raises(ValueError, match="act_dtype"):
+        moe.moe_block_norm(d["residual"], pre_weight=d["pre_weight"], out=(None, n.half(), None, rstd))
