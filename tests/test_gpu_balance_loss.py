@@ -433,3 +433,17 @@ def test_outputs_under_another_default_type():
         torch.set_default_dtype(F32)
     assert all(got[k].dtype == want[k].dtype and torch.equal(got[k], want[k]) for k in want)
     assert torch.equal(grad, gwant)
+
+
+@pytest.mark.parametrize("T,E,S", [(32768, 256, 1), (40000, 61, 3), (64, 16, 1), (3000, 1000, 8), (20000, 32, 200)])
+def test_without_the_means(T, E, S):
+    """Outputs without prob_mean, in one, two and three launches, and a workspace of exactly the bytes asked for."""
+    cuts = [T * i // S for i in range(S + 1)]
+    d = _gpu(_inputs(T, E, 4, cuts=cuts, seed=S))
+    want = moe.moe_balance_loss(d["logits"], d["topk_idx"], seq_offsets=d["seq_offsets"])
+    out = {k: torch.empty_like(v) for k, v in want.items() if k != "prob_mean"}
+    need = moe.moe_balance_loss_workspace_bytes(T, E, S)
+    ws = torch.full((need + 4096,), 0xFF, dtype=torch.uint8, device="cuda")
+    moe.moe_balance_loss(d["logits"], d["topk_idx"], seq_offsets=d["seq_offsets"], out=out, workspace=ws[:need])
+    assert all(torch.equal(out[k], want[k]) for k in out)
+    assert (ws[need:] == 0xFF).all()
