@@ -30,7 +30,12 @@
  *   block with its gate and the residual scale, and their gradients;
  *   moe_expert_matvec: a few rows per expert times its 4-bit weights;
  *   moe_balance_loss, moe_balance_loss_backward: the router's balance loss,
- *   per-expert counts and gradient over packed sequences.
+ *   per-expert counts and gradient over packed sequences;
+ *   moe_router, moe_router_backward: the routing from the router's logits
+ *   (scores, a bias for balance, groups, top-k, weights), and its gradient;
+ *   moe_cast_int8, swiglu_cast_int8, moe_expert_matmul_int8: rows and SwiGLU's
+ *   result as 8-bit integers with one scale a row, and the experts' products
+ *   of such rows with 8-bit weights, from one row to a prompt's.
  *
  * Device-side checks of the inputs' preconditions, for debugging:
  *   moe_check_scores, moe_check_topk_idx, moe_check_pos,
@@ -635,6 +640,144 @@ moe_status moe_expert_matvec(const void* x, int32_t x_dtype, const float* x_sf, 
                              int32_t num_experts, const int32_t* expert_offsets, const uint8_t* w_codes,
                              const void* w_sf, int32_t group_size, int32_t sf_ue8m0, uint16_t* out_bf16,
                              hipStream_t stream);
+
+#define MOE_GROUP_MAX 0  /* a group's score is its best expert's */
+#define MOE_GROUP_TOP2 1 /* the sum of its two best experts' */
+#define MOE_ROUTER_MAX_GROUPS 64
+
+/*
+ * moe_router -- the routing of each token from the router's logits.
+ *
+ * With s[t, :] the scores of token t, the softmax (MOE_SCORE_SOFTMAX) or the
+ * sigmoids (MOE_SCORE_SIGMOID; not divided by their sum) of its logits, and
+ * c[t, e] = s[t, e] + bias[e]:
+ *   - the experts lie in num_groups groups of E / num_groups consecutive ones;
+ *     the topk_groups groups with the largest scores are taken, a group's
+ *     score being the largest c of its experts or the sum of its two largest;
+ *   - topk_idx[t, :] are the K experts of those groups with the largest c, in
+ *     descending order;
+ *   - topk_weights[t, k] = scale * s[t, topk_idx[t, k]], with renormalize = 1
+ *     divided by the sum of the K scores.  The bias has no part in them.
+ * Equal values go to the lowest index.  Values are ordered as 64-bit numbers
+ * hold them, with no bias and MOE_GROUP_MAX as the logits themselves are;
+ * weights are computed in fp32, renormalised ones without underflow whatever
+ * the logits.
+ *
+ * An expert whose logit is -inf or NaN, or whose bias is -inf or NaN, is not
+ * taken; a logit or bias of +inf counts as the largest finite number.  Where
+ * no expert is left for a round, its id is -1 and its weight 0 (moe_token_map
+ * leaves such copies out).  So are all of a masked token's.
+ *
+ * logits         logits_dtype [T, E], rows row_stride elements apart.
+ * logits_dtype   MOE_DTYPE_BF16 or MOE_DTYPE_F32.
+ * num_tokens     0 <= T <= (2^31 - 1) / 16.
+ * num_experts    E, 1 <= E <= 1024.
+ * num_topk       K, 1 <= K <= min(16, topk_groups * E / num_groups).
+ * bias           fp32 [E], or NULL.
+ * num_groups     divides E; at most MOE_ROUTER_MAX_GROUPS (above:
+ *                MOE_ERR_UNSUPPORTED).  1: no groups.
+ * topk_groups    1 <= topk_groups <= num_groups.
+ * group_score    MOE_GROUP_MAX or MOE_GROUP_TOP2 (with more than one group it
+ *                needs groups of at least two experts).
+ * scale          finite.
+ * token_mask     uint8 [T], 0 = masked (the token's logits may hold anything;
+ *                their memory is still read), or NULL.
+ * topk_idx       int64 [T, K] output;  topk_weights fp32 [T, K] output.
+ */
+moe_status moe_router(const void* logits, int32_t logits_dtype, int64_t row_stride, int64_t num_tokens,
+                      int32_t num_experts, int32_t num_topk, int32_t score, const float* bias, int32_t num_groups,
+                      int32_t topk_groups, int32_t group_score, int32_t renormalize, float scale,
+                      const uint8_t* token_mask, int64_t* topk_idx, float* topk_weights, hipStream_t stream);
+
+/*
+ * moe_router_backward -- the gradient of the weights that moe_router gives
+ * with respect to the logits (the choice of the experts carries none).  With
+ * g = scale * grad_weights[t, :], s the scores, and over the chosen experts
+ * p_k = s_k / sum_j s_j:
+ *   renormalize = 1: p_k (g_k - sum_j p_j g_j)  [* (1 - s_k) for sigmoid],
+ *   renormalize = 0, sigmoid: g_k s_k (1 - s_k)
+ * at the chosen experts, 0 at the others;
+ *   renormalize = 0, softmax: s_e (g_e - sum_j s_j g_j) for every expert e,
+ * g_e being 0 for those not chosen.  In fp32, rounded once.
+ *
+ * grad_weights   fp32 [T, K].
+ * topk_idx       int64 [T, K] from moe_router: the ids of a row distinct; an
+ *                id outside [0, E) takes no part (its gradient is not used).
+ * grad_logits    logits_dtype [T, E] contiguous output; a masked token's row,
+ *                whose ids are all -1, becomes 0.
+ * The others as for moe_router.
+ */
+moe_status moe_router_backward(const float* grad_weights, const void* logits, int32_t logits_dtype,
+                               int64_t row_stride, int64_t num_tokens, int32_t num_experts, const int64_t* topk_idx,
+                               int32_t num_topk, int32_t score, int32_t renormalize, float scale, void* grad_logits,
+                               hipStream_t stream);
+
+/*
+ * moe_cast_int8 -- rows as 8-bit integers with one scale a row:
+ *   sf[r]      = max(max over the row of |x|, 127 * 2^-126) / 127
+ *   out[r, i]  = round(x[r, i] * (1 / sf[r])), to nearest, ties to even,
+ * every operation rounded once in fp32; codes lie in [-127, 127].  The
+ * activations have to be finite.
+ *
+ * x              x_dtype [num_rows, width], rows row_stride elements apart.
+ * x_dtype        MOE_DTYPE_BF16 or MOE_DTYPE_F32.
+ * num_rows       0 <= R < 2^24 (above: MOE_ERR_UNSUPPORTED).
+ * width          1 <= width <= MOE_MATVEC_MAX_WIDTH (above:
+ *                MOE_ERR_UNSUPPORTED).
+ * out            int8 [R, width] output;  out_sf fp32 [R] output.
+ */
+moe_status moe_cast_int8(const void* x, int32_t x_dtype, int64_t row_stride, int64_t num_rows, int32_t width,
+                         int8_t* out, float* out_sf, hipStream_t stream);
+
+/*
+ * swiglu_cast_int8 -- swiglu_cast with moe_cast_int8's format: of
+ *   v[r, i] = (l / (1 + exp(-l))) * u * row_weights[r],
+ * l = gate_up[r, i], u = gate_up[r, inter + i], clamped first where
+ * clamp_value > 0 (l = min(l, c), u = max(min(u, c), -c)), the codes and the
+ * row's scale.  The activations have to be finite.
+ *
+ * gate_up_bf16   bf16 [num_rows, 2 * inter], any alignment of 2 bytes.
+ * num_rows, inter   as num_rows and width of moe_cast_int8.
+ * row_weights    fp32 [num_rows] or NULL.
+ * out            int8 [R, inter] output;  out_sf fp32 [R] output.
+ */
+moe_status swiglu_cast_int8(const uint16_t* gate_up_bf16, int64_t num_rows, int32_t inter, const float* row_weights,
+                            float clamp_value, int8_t* out, float* out_sf, hipStream_t stream);
+
+#define MOE_MATMUL_INT8_MAX_INNER 131071 /* 2^31 over the largest product of two codes, 2^14 */
+#define MOE_MATMUL_INT8_MAX_TILES 16777216 /* of 16 rows and 64 channels: a launch's workgroups */
+
+/*
+ * moe_expert_matmul_int8 -- the experts' products in 8-bit integers: rows
+ * grouped by expert, any number per expert, times that expert's weights.
+ *
+ *   out[r, n] = (fp32(sum over k of x[r', k] * w[e, n, k]) * x_sf[r']) * w_sf[e, n]
+ * for the rows r of expert e, expert_offsets[e] <= r < expert_offsets[e + 1],
+ * with r' = row_token[r] if given (the token rows themselves, without an
+ * expand) and r otherwise.  The sum is exact; it, the two products and the
+ * output round once each.  A row whose row_token is outside [0, x_rows) gets
+ * zeros; rows of no expert are not written.
+ *
+ * x              int8 [x_rows, inner], x_sf fp32 [x_rows] (moe_cast_int8,
+ *                swiglu_cast_int8).
+ * row_token      int32 [num_rows], or NULL (then x_rows == num_rows, unless
+ *                num_rows is 0).
+ * num_rows       R >= 0.
+ * inner          1 <= inner <= MOE_MATMUL_INT8_MAX_INNER, out_width N <=
+ *                MOE_MATVEC_MAX_WIDTH, (R / 16 + E) * ceil(N / 64) below
+ *                MOE_MATMUL_INT8_MAX_TILES (else: MOE_ERR_UNSUPPORTED).
+ * num_experts    E, 1 <= E <= 1024.
+ * expert_offsets int32 [E + 1], non-decreasing, within [0, R] (from
+ *                moe_token_map); NULL for E == 1: all rows.
+ * w              int8 [E, N, inner], w_sf fp32 [E, N].
+ * out_dtype      MOE_DTYPE_BF16 or MOE_DTYPE_F32;  out [R, N] output.
+ * x and w may have any alignment; inner a multiple of 16 with both 16-byte
+ * aligned is the fast form.
+ */
+moe_status moe_expert_matmul_int8(const int8_t* x, const float* x_sf, int64_t x_rows, const int32_t* row_token,
+                                  int64_t num_rows, int32_t inner, int32_t out_width, int32_t num_experts,
+                                  const int32_t* expert_offsets, const int8_t* w, const float* w_sf,
+                                  int32_t out_dtype, void* out, hipStream_t stream);
 
 /* moe_route modes */
 #define MOE_ROUTE_AUTO 0  /* the local form up to 16 tokens; the fused form when the batch has more than

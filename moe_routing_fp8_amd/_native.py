@@ -74,6 +74,12 @@ _SIGNATURES = {
                                   ctypes.c_int),
     "moe_expert_matvec": ([_p, _i32, _p, _i64, _p, _i64, _i32, _i32, _i32, _p, _p, _p, _i32, _i32, _p, _p],
                           ctypes.c_int),
+    "moe_router": ([_p, _i32, _i64, _i64, _i32, _i32, _i32, _p, _i32, _i32, _i32, _i32, _f32, _p, _p, _p, _p],
+                   ctypes.c_int),
+    "moe_router_backward": ([_p, _p, _i32, _i64, _i64, _i32, _p, _i32, _i32, _i32, _f32, _p, _p], ctypes.c_int),
+    "moe_cast_int8": ([_p, _i32, _i64, _i64, _i32, _p, _p, _p], ctypes.c_int),
+    "swiglu_cast_int8": ([_p, _i64, _i32, _p, _f32, _p, _p, _p], ctypes.c_int),
+    "moe_expert_matmul_int8": ([_p, _p, _i64, _p, _i64, _i32, _i32, _i32, _p, _p, _p, _i32, _p, _p], ctypes.c_int),
     "moe_check_scores": ([_p, _i64, _i32, _i32, _p, _p], ctypes.c_int),
     "moe_check_topk_idx": ([_p, _i64, _i32, _i32, _p, _p], ctypes.c_int),
     "moe_check_pos_workspace_bytes": ([_i64], _sz),
@@ -103,6 +109,9 @@ MOE_GATE_TOKEN = 2
 
 MOE_SCORE_SOFTMAX = 0
 MOE_SCORE_SIGMOID = 1
+
+MOE_GROUP_MAX = 0
+MOE_GROUP_TOP2 = 1
 
 MOE_DISPATCH_AUTO = 0
 MOE_DISPATCH_SINGLE_LAUNCH = 1
@@ -1067,4 +1076,144 @@ def moe_expert_matvec(x: torch.Tensor, w_codes: torch.Tensor, w_sf: torch.Tensor
         _need_out(out, torch.bfloat16, (R, N), "out", dev)
     _call("moe_expert_matvec", dev, stream, _ptr(x), MOE_DTYPE_E4M3 if e4m3 else MOE_DTYPE_BF16, _ptr(x_sf), X,
           _ptr(row_token), R, K, N, E, _ptr(expert_offsets), _ptr(w_codes), _ptr(w_sf), K // G, int(ue8m0), _ptr(out))
+    return out
+
+
+_GROUP_SCORES = {"max": MOE_GROUP_MAX, "top2": MOE_GROUP_TOP2}
+
+
+def moe_router(logits: torch.Tensor, num_topk: int, score: str = "softmax", bias: Optional[torch.Tensor] = None,
+               num_groups: int = 1, topk_groups: int = 1, group_score: str = "max", renormalize: bool = False,
+               scale: float = 1.0, token_mask: Optional[torch.Tensor] = None, out=None,
+               stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """The routing from the router's logits bf16 or fp32 [T, E] (any row stride): the `num_topk` experts with the
+    largest score + bias among the `topk_groups` best of `num_groups` groups, in descending order, and their scores
+    times `scale` (`renormalize`: divided by their sum) -> (topk_idx int64 [T, K], topk_weights fp32 [T, K]).
+    `score`: "softmax" or "sigmoid"; bias fp32 [E]; `group_score`: a group's best score + bias ("max") or the sum of
+    its two best ("top2").  token_mask bool [T]: a token that is False gets ids -1 and weights 0, as does a round for
+    which no expert is left (logits of -inf or NaN are none).  Nothing is recorded for autograd: the gradient comes
+    from moe_router_backward."""
+    stride, mode, _ = _balance_inputs(logits, score, token_mask, None)
+    T, E = logits.shape
+    dev = logits.device
+    _need_param(bias, E, "bias", dev)
+    if group_score not in _GROUP_SCORES:
+        raise ValueError(f"group_score: expected one of {sorted(_GROUP_SCORES)}, got {group_score!r}")
+    if out is None:
+        with _alloc_on(stream):
+            out = (torch.empty((T, num_topk), dtype=torch.int64, device=dev),
+                   torch.empty((T, num_topk), dtype=torch.float32, device=dev))
+    else:
+        _need_out(out[0], torch.int64, (T, num_topk), "topk_idx", dev)
+        _need_out(out[1], torch.float32, (T, num_topk), "topk_weights", dev)
+    _call("moe_router", dev, stream, _ptr(logits), _NORM_DTYPES[logits.dtype], stride, T, E, num_topk, mode,
+          _ptr(bias), num_groups, topk_groups, _GROUP_SCORES[group_score], int(bool(renormalize)), float(scale),
+          _ptr(token_mask), _ptr(out[0]), _ptr(out[1]))
+    return out
+
+
+def moe_router_backward(grad_weights: torch.Tensor, logits: torch.Tensor, topk_idx: torch.Tensor,
+                        score: str = "softmax", renormalize: bool = False, scale: float = 1.0,
+                        out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """The gradient of sum(grad_weights * topk_weights) with respect to the logits of moe_router, in their type
+    [T, E]; grad_weights fp32 [T, K], topk_idx from moe_router (a row's ids distinct; ids of -1 take no part)."""
+    stride, mode, _ = _balance_inputs(logits, score, None, None)
+    T, E = logits.shape
+    dev = logits.device
+    if topk_idx.dim() != 2:
+        raise ValueError(f"topk_idx: expected a 2-d tensor, got {tuple(topk_idx.shape)}")
+    K = topk_idx.shape[1]
+    _need_out(topk_idx, torch.int64, (T, K), "topk_idx", dev)
+    _need_out(grad_weights, torch.float32, (T, K), "grad_weights", dev)
+    if out is None:
+        with _alloc_on(stream):
+            out = torch.empty((T, E), dtype=logits.dtype, device=dev)
+    else:
+        _need_out(out, logits.dtype, (T, E), "out", dev)
+    _call("moe_router_backward", dev, stream, _ptr(grad_weights), _ptr(logits), _NORM_DTYPES[logits.dtype], stride, T,
+          E, _ptr(topk_idx), K, mode, int(bool(renormalize)), float(scale), _ptr(out))
+    return out
+
+
+def _int8_outputs(R, width, dev, out, stream):
+    if out is None:
+        with _alloc_on(stream):
+            return (torch.empty((R, width), dtype=torch.int8, device=dev),
+                    torch.empty(R, dtype=torch.float32, device=dev))
+    _need_out(out[0], torch.int8, (R, width), "out", dev)
+    _need_out(out[1], torch.float32, (R,), "out_sf", dev)
+    return out
+
+
+def moe_cast_int8(x: torch.Tensor, out=None, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Rows bf16 or fp32 [R, H] (any row stride) -> (codes int8 [R, H], scales fp32 [R]): one scale a row, its
+    largest magnitude / 127."""
+    stride = _need_rows(x, "x")
+    R, H = x.shape
+    dev = x.device
+    o = _int8_outputs(R, H, dev, out, stream)
+    if debug_enabled() and x.dtype == torch.bfloat16 and x.is_contiguous():
+        _debug_raise("moe_cast_int8", lambda: moe_check_activations(x, stream=stream), stream)
+    _call("moe_cast_int8", dev, stream, _ptr(x), _NORM_DTYPES[x.dtype], stride, R, H, _ptr(o[0]), _ptr(o[1]))
+    return o
+
+
+def swiglu_cast_int8(gate_up: torch.Tensor, row_weights: Optional[torch.Tensor] = None, clamp_value: float = 0.0,
+                     out=None, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """SwiGLU of bf16 [R, 2 * I] times the row weights fp32 [R] -> (codes int8 [R, I], scales fp32 [R]), one scale a
+    row."""
+    _need(gate_up, torch.bfloat16, 2, "gate_up")
+    R, two_i = gate_up.shape
+    if two_i % 2:
+        raise ValueError("gate_up: last dimension must be 2 * inter")
+    inter = two_i // 2
+    dev = gate_up.device
+    _need_param(row_weights, R, "row_weights", dev)
+    o = _int8_outputs(R, inter, dev, out, stream)
+    if debug_enabled():
+        _debug_raise("swiglu_cast_int8", lambda: moe_check_activations(gate_up, stream=stream), stream)
+    _call("swiglu_cast_int8", dev, stream, _ptr(gate_up), R, inter, _ptr(row_weights), float(clamp_value), _ptr(o[0]),
+          _ptr(o[1]))
+    return o
+
+
+def moe_expert_matmul_int8(x: torch.Tensor, x_sf: torch.Tensor, w: torch.Tensor, w_sf: torch.Tensor,
+                           expert_offsets: Optional[torch.Tensor] = None, row_token: Optional[torch.Tensor] = None,
+                           out_dtype: Optional[torch.dtype] = None, out: Optional[torch.Tensor] = None,
+                           stream=None) -> torch.Tensor:
+    """Rows grouped by expert times 8-bit weights: x int8 [X, K] with x_sf fp32 [X] (moe_cast_int8), w int8 [E, N, K]
+    ([N, K] for one matrix) with w_sf fp32 [E, N]; expert_offsets int32 [E+1] (None: one matrix, all rows); row_token
+    int32 [R] to read row r from x[row_token[r]] (None: R == X) -> [R, N] in `out_dtype`, bf16 or fp32 (by default
+    that of `out`, or bf16).  Rows of no expert are not written."""
+    if x.dtype != torch.int8 or x.dim() != 2 or not x.is_contiguous():
+        raise ValueError(f"x: expected a contiguous 2-d int8 tensor, got {x.dtype} {tuple(x.shape)}")
+    dev = x.device
+    X, K = x.shape
+    if w.dim() == 2:
+        w, w_sf = w.unsqueeze(0), w_sf.unsqueeze(0)
+    if w.dim() != 3:
+        raise ValueError(f"w: expected a [E, N, K] tensor, got {tuple(w.shape)}")
+    E, N, _ = w.shape
+    _need_out(w, torch.int8, (E, N, K), "w", dev)
+    _need_out(w_sf, torch.float32, (E, N), "w_sf", dev)
+    _need_out(x_sf, torch.float32, (X,), "x_sf", dev)
+    if expert_offsets is not None:
+        _need_out(expert_offsets, torch.int32, (E + 1,), "expert_offsets", dev)
+    elif E != 1:
+        raise ValueError("expert_offsets: required with more than one expert")
+    R = X
+    if row_token is not None:
+        R = row_token.numel()
+        _need_out(row_token, torch.int32, (R,), "row_token", dev)
+    if out_dtype is None:
+        out_dtype = torch.bfloat16 if out is None else out.dtype
+    if out_dtype not in _NORM_DTYPES:
+        raise ValueError(f"out_dtype: expected bf16 or fp32, got {out_dtype}")
+    if out is None:
+        with _alloc_on(stream):
+            out = torch.empty((R, N), dtype=out_dtype, device=dev)
+    else:
+        _need_out(out, out_dtype, (R, N), "out", dev)
+    _call("moe_expert_matmul_int8", dev, stream, _ptr(x), _ptr(x_sf), X, _ptr(row_token), R, K, N, E,
+          _ptr(expert_offsets), _ptr(w), _ptr(w_sf), _NORM_DTYPES[out_dtype], _ptr(out))
     return out
