@@ -3,11 +3,11 @@
 //   out[r, n] = (fp32(sum_k x[r', k] * w[e, n, k]) * x_sf[r']) * w_sf[e, n].
 // The sums are whole numbers in 32 bits, exact in any order.
 //
-// One workgroup computes a tile of BM rows of one expert and BN channels.  The
+// A workgroup computes tiles of up to BM rows of one expert by BN channels.  The
 // x rows and w rows of BK bytes of k go from memory to LDS without passing
-// registers (16 bytes a lane, 1024 consecutive LDS bytes a wave), STAGES steps
-// of k in flight; the matrix instruction takes 16 rows of each with 64 bytes
-// of k from there.
+// registers (16 bytes a lane, 1024 consecutive LDS bytes a wave), one or two steps of
+// k ahead; the matrix instruction takes 16 rows of each with 64 bytes of k from
+// there.
 #include <hip/hip_runtime.h>
 
 #include "api_common.hpp"
@@ -36,36 +36,28 @@ struct MatmulArgs {
     const uint8_t* w;
     const float* w_sf;
     void* out;
-    int out_f32, vec4;  // vec4: four channels are stored at once
+    int out_f32, vec;  // vec: channels that lie side by side are stored at once
     int n_tiles;
 };
 
 __device__ const uint4 kZeroChunk = {0, 0, 0, 0};
 
-// Where the 16-byte chunk c of row r lies in its row of a stage: rows that a
-// matrix instruction's lanes read together have it in different banks.
-template <int BK>
-__device__ __forceinline__ int swizzle(int r, int c) {
-    return c ^ (r & (BK / 16 - 1));
-}
+// The tile's place: BM rows of an expert, BN channels.
+struct Tile {
+    int expert;
+    int rows;     // rows of the tile
+    int channel;  // first channel
+    int64_t row;  // first row
+};
 
-template <int N>
-__device__ __forceinline__ void wait_loads() {
-    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(N) : "memory");
-}
-
-__device__ __forceinline__ int row_tiles(const MatmulArgs& a, int e, int bm, int64_t& begin, int64_t& count) {
-    if (a.expert_offsets == nullptr) {
-        begin = 0;
-        count = a.num_rows;
-    } else {
-        int64_t b = a.expert_offsets[e], c = a.expert_offsets[e + 1];
-        b = b < 0 ? 0 : b > a.num_rows ? a.num_rows : b;
-        c = c < b ? b : c > a.num_rows ? a.num_rows : c;
-        begin = b;
-        count = c - b;
-    }
-    return static_cast<int>((count + bm - 1) / bm);
+// The rows of expert e, whatever the offsets hold within [0, num_rows].
+__device__ __forceinline__ void expert_rows(const MatmulArgs& a, int e, int& begin, int& count) {
+    begin = 0;
+    count = static_cast<int>(a.num_rows);
+    if (a.expert_offsets == nullptr) return;
+    const int most = static_cast<int>(a.num_rows);
+    begin = min(max(a.expert_offsets[e], 0), most);
+    count = min(max(a.expert_offsets[e + 1], begin), most) - begin;
 }
 
 // Inclusive sum over the wave's lanes.
@@ -78,58 +70,431 @@ __device__ __forceinline__ int wave_scan(int v, int lane) {
     return v;
 }
 
-struct Tile {
-    int expert;
-    int64_t row;   // first row
-    int rows;      // rows of the tile
-    int channel;   // first channel
+// Numbers the tiles expert by expert: an expert's rows are shared evenly, in
+// whole blocks of 16, by as few tiles of up to BM rows as hold them.  Within an
+// expert, kGroupTiles row tiles of one channel tile after another, so that tiles
+// that run together share rows of w and x.  Every wave holds the sums of each
+// lane's experts, and finds the same tiles by itself.
+template <int BM, int BN>
+struct Tiles {
+    const MatmulArgs& a;
+    int lane, chunk;        // experts a lane
+    int begin, count;       // the lane's expert, if chunk is 1
+    int mine, weight;       // row tiles of the lane's experts, and what they cost
+    int tiles_to, cost_to;  // the same up to and with this lane's
+    int total, cost;        // of all experts
+
+    static __device__ __forceinline__ int row_tiles(int count) { return (count + BM - 1) / BM; }
+    static __device__ __forceinline__ int tile_rows(int count, int tiles) {
+        return tiles == 0 ? 0 : ((count + tiles - 1) / tiles + 15) / 16 * 16;
+    }
+    // A tile's time, in sixteenths of what its rows add: its loads take about as long as half of them.
+    static __device__ __forceinline__ int tile_cost(int rows) { return (rows + BM / 2) / 16 + 1; }
+
+    __device__ __forceinline__ explicit Tiles(const MatmulArgs& args)
+        : a(args), lane(threadIdx.x % kWave), chunk((args.E + kWave - 1) / kWave), begin(0), count(0), mine(0),
+          weight(0) {
+        for (int i = 0; i < chunk; ++i) {
+            const int e = lane * chunk + i;
+            if (e >= a.E) continue;
+            expert_rows(a, e, begin, count);
+            const int n = row_tiles(count);
+            mine += n;
+            weight += n * tile_cost(tile_rows(count, n));
+        }
+        tiles_to = wave_scan(mine, lane);
+        cost_to = wave_scan(weight, lane);
+        total = __builtin_amdgcn_readlane(tiles_to, kWave - 1);
+        cost = __builtin_amdgcn_readlane(cost_to, kWave - 1);
+    }
+
+    // An expert, and the row tiles and their cost before it.
+    struct Found {
+        int expert, begin, count, tiles_before, cost_before;
+    };
+    // The expert at which the sum picked by `value` passes `at`, 0 <= at < its total.
+    template <typename V>
+    __device__ __forceinline__ Found search(int at, V value) const {
+        const int to = value(tiles_to, cost_to);
+        int owner = __popcll(__ballot(to <= at));
+        Found f;
+        f.expert = owner;
+        f.tiles_before = __builtin_amdgcn_readlane(tiles_to - mine, owner);
+        f.cost_before = __builtin_amdgcn_readlane(cost_to - weight, owner);
+        int first = begin, rows = count;
+        if (chunk > 1) {
+            const int e = owner * chunk + lane;
+            int n = 0, c = 0;
+            first = rows = 0;
+            if (lane < chunk && e < a.E) {
+                expert_rows(a, e, first, rows);
+                n = row_tiles(rows);
+                c = n * tile_cost(tile_rows(rows, n));
+            }
+            const int n_to = f.tiles_before + wave_scan(n, lane), c_to = f.cost_before + wave_scan(c, lane);
+            const int in = __popcll(__ballot(value(n_to, c_to) <= at));
+            f.expert = owner * chunk + in;
+            f.tiles_before = __builtin_amdgcn_readlane(n_to - n, in);
+            f.cost_before = __builtin_amdgcn_readlane(c_to - c, in);
+            owner = in;
+        }
+        f.begin = __builtin_amdgcn_readlane(first, owner);
+        f.count = __builtin_amdgcn_readlane(rows, owner);
+        return f;
+    }
+
+    // The first tile of part `part` of `parts` of about the same cost.
+    __device__ __forceinline__ int64_t start_of(int part, int parts) const {
+        if (part >= parts || total == 0) return static_cast<int64_t>(total) * a.n_tiles;
+        const int64_t target = static_cast<int64_t>(cost) * a.n_tiles * part / parts;
+        const Found f = search(static_cast<int>(target / a.n_tiles), [](int, int c) { return c; });
+        const int64_t into = target - static_cast<int64_t>(f.cost_before) * a.n_tiles;
+        return static_cast<int64_t>(f.tiles_before) * a.n_tiles +
+               into / tile_cost(tile_rows(f.count, row_tiles(f.count)));
+    }
+
+    // Tile number id, 0 <= id < total * n_tiles.
+    __device__ __forceinline__ Tile find(int64_t id) const {
+        const Found f = search(static_cast<int>(id / a.n_tiles), [](int n, int) { return n; });
+        const int m_tiles = row_tiles(f.count), rows = tile_rows(f.count, m_tiles);
+        const int64_t local = id - static_cast<int64_t>(f.tiles_before) * a.n_tiles;
+        const int64_t per_group = static_cast<int64_t>(kGroupTiles) * a.n_tiles;
+        const int g = static_cast<int>(local / per_group);
+        const int in_group = static_cast<int>(local - g * per_group);
+        const int width = min(kGroupTiles, m_tiles - g * kGroupTiles);
+        const int n = in_group / width, m = g * kGroupTiles + in_group % width;
+        Tile t;
+        t.expert = f.expert;
+        t.rows = min(rows, f.count - m * rows);
+        t.channel = n * BN;
+        t.row = static_cast<int64_t>(f.begin) + static_cast<int64_t>(m) * rows;
+        return t;
+    }
 };
 
-// The workgroup's tile.  Tiles are numbered expert by expert; within an
-// expert, kGroupTiles row tiles of one channel tile after another, so that
-// tiles that run together share rows of w and x.  Each die takes a run of
-// consecutive tiles.  Every wave finds the same tile by itself.
-template <int BM, int BN>
-__device__ __forceinline__ bool find_tile(const MatmulArgs& a, Tile& t) {
-    const int lane = threadIdx.x % kWave;
-    const int chunk = (a.E + kWave - 1) / kWave;
-    int64_t begin, count;
-    int mine = 0;
-    for (int i = 0; i < chunk; ++i) {
-        const int e = lane * chunk + i;
-        if (e < a.E) mine += row_tiles(a, e, BM, begin, count);
+// How a tile's products lie over the waves and lanes, and its rows in LDS.
+//
+// A wave multiplies TM x TN blocks of 16 rows by 16 channels.  Its row blocks
+// are WM apart, so that a tile that is not full leaves all waves an equal share.
+// Lane l holds, of each block, row l % 16 and four channels, those of block
+// 2 j + 1 next to those of block 2 j: eight channels in a row, 64 bytes of four
+// lanes, are stored together.
+//
+// LDS holds the BM rows of x and the BN rows of w, BK bytes each.  The 16-byte
+// chunk c of a row lies at c ^ swizzle(row): eight or sixteen consecutive lanes,
+// which read together, have it in different banks.
+template <int BM, int BN, int BK, int WM, int WN>
+struct Layout {
+    static constexpr int kWaves = WM * WN;
+    static constexpr int kChunks = BK / 16;
+    static constexpr int kRowsPerLoad = kWave / kChunks;  // rows that a wave's 1024-byte load covers
+    static constexpr int kXLoads = BM / kRowsPerLoad, kWLoads = BN / kRowsPerLoad;  // of a step, all waves together
+    static constexpr int TM = BM / WM / 16, TN = BN / WN / 16;
+    static constexpr bool kPairs = TN % 2 == 0;
+    static_assert(BM % kRowsPerLoad == 0 && BN % (kRowsPerLoad * kWaves) == 0 && BM % (16 * WM) == 0 &&
+                      BN % (16 * WN) == 0, "tile");
+    typedef i32x4_t Sums[TM][TN];
+
+    static __device__ __forceinline__ int x_swizzle(int r) { return r & (kChunks - 1); }
+    static __device__ __forceinline__ int w_swizzle(int r) {
+        return (kPairs ? (r & 3) | ((r >> 3) & 3) << 2 : r) & (kChunks - 1);
     }
-    int incl = wave_scan(mine, lane);
-    const int total = __builtin_amdgcn_readlane(incl, kWave - 1);
-    const int64_t tiles = static_cast<int64_t>(total) * a.n_tiles;
-    const int64_t per = (tiles + kXcds - 1) / kXcds;
-    const int64_t turn = blockIdx.x / kXcds;
-    const int64_t id = (blockIdx.x % kXcds) * per + turn;
-    if (turn >= per || id >= tiles) return false;
-    const int slot = static_cast<int>(id / a.n_tiles);
-    int owner = __popcll(__ballot(incl <= slot));
-    int before = __builtin_amdgcn_readlane(incl - mine, owner);
-    int e = owner;
-    if (chunk > 1) {
-        const int first = owner * chunk;
-        mine = lane < chunk && first + lane < a.E ? row_tiles(a, first + lane, BM, begin, count) : 0;
-        incl = before + wave_scan(mine, lane);
-        owner = __popcll(__ballot(incl <= slot));
-        before = __builtin_amdgcn_readlane(incl - mine, owner);
-        e = first + owner;
+    // channel of a wave's block n that line i (0 to 15) of the instruction has
+    static __device__ __forceinline__ int channel(int n, int i) {
+        return kPairs ? n / 2 * 32 + i / 4 * 8 + n % 2 * 4 + i % 4 : n * 16 + i;
     }
-    const int m_tiles = row_tiles(a, e, BM, begin, count);
-    const int64_t local = id - static_cast<int64_t>(before) * a.n_tiles;
-    const int64_t per_group = static_cast<int64_t>(kGroupTiles) * a.n_tiles;
-    const int g = static_cast<int>(local / per_group);
-    const int in_group = static_cast<int>(local - g * per_group);
-    const int width = min(kGroupTiles, m_tiles - g * kGroupTiles);
-    const int n = in_group / width, m = g * kGroupTiles + in_group % width;
-    t.expert = e;
-    t.row = begin + static_cast<int64_t>(m) * BM;
-    t.rows = static_cast<int>(min<int64_t>(BM, count - static_cast<int64_t>(m) * BM));
-    t.channel = n * BN;
-    return true;
+
+    // Adds the products of one step for the wave's first `used` row blocks.  Each
+    // block's rows of x are read two blocks before they are multiplied, the next
+    // 64 bytes of w along with them; the scheduler, left alone, reads them just
+    // before (32 experts, 16384 rows: 612 against 596 us).
+    static __device__ __forceinline__ void multiply(const uint8_t* x, const uint8_t* w, int used, int wm, int wn,
+                                                    int lane, Sums& acc) {
+        constexpr int U = BK / 64, kAhead = 2, kHeld = kAhead + 1;
+        const int line = lane % 16;
+        const int x_row = wm * 16 + line, w_row = wn * (BN / WN) + channel(0, line);
+        auto read_x = [&](int i) {
+            const int c = (i / TM * 4 + lane / 16) ^ x_swizzle(x_row);  // all the wave's rows of a line have one swizzle
+            return *reinterpret_cast<const i32x4_t*>(x + (x_row + i % TM * WM * 16) * BK + c * 16);
+        };
+        auto read_w = [&](int k, int n) {
+            const int row = w_row + channel(n, 0), c = (k * 4 + lane / 16) ^ w_swizzle(row);
+            return *reinterpret_cast<const i32x4_t*>(w + row * BK + c * 16);
+        };
+        i32x4_t xf[kHeld], wf[2][TN];
+#pragma unroll
+        for (int n = 0; n < TN; ++n) wf[0][n] = read_w(0, n);
+#pragma unroll
+        for (int i = 0; i < kAhead && i < U * TM; ++i) xf[i] = read_x(i);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int i = 0; i < U * TM; ++i) {
+            const int k = i / TM, m = i % TM;
+            if (i + kAhead < U * TM) xf[(i + kAhead) % kHeld] = read_x(i + kAhead);
+#pragma unroll
+            for (int n = 0; n < TN; ++n)
+                if (k + 1 < U && n * TM / TN == m) wf[(k + 1) % 2][n] = read_w(k + 1, n);
+            if (m < used) {
+#pragma unroll
+                for (int n = 0; n < TN; ++n)
+                    acc[m][n] =
+                        __builtin_amdgcn_mfma_i32_16x16x64_i8(wf[k % 2][n], xf[i % kHeld], acc[m][n], 0, 0, 0);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    }
+    // The row blocks of wave row wm that a tile of `rows` rows reaches.
+    static __device__ __forceinline__ int used_blocks(int rows, int wm) {
+        return max((rows + 15) / 16 - wm + WM - 1, 0) / WM;
+    }
+
+    // Writes the wave's results.  xs(r) gives a row's scale and whether it has
+    // one, ws(c) a channel's.
+    template <typename XS, typename WS>
+    static __device__ __forceinline__ void store(const MatmulArgs& a, const Tile& t, int wm, int wn, int lane,
+                                                 const Sums& acc, XS xs, WS ws) {
+        constexpr int V = kPairs ? 8 : 4;  // channels that lie side by side
+        const int c0 = wn * (BN / WN) + lane / 16 * V;
+#pragma unroll
+        for (int n = 0; n < TN; n += V / 4) {
+            const int c = c0 + channel(n, 0);
+            float scale[V];
+#pragma unroll
+            for (int i = 0; i < V; ++i) scale[i] = ws(c + i);
+#pragma unroll
+            for (int m = 0; m < TM; ++m) {
+                const int r = (m * WM + wm) * 16 + lane % 16;
+                if (r >= t.rows || t.channel + c >= a.N) continue;
+                bool known;
+                const float x_scale = xs(r, known);
+                float v[V];
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    v[i] = static_cast<float>(acc[m][n + i / 4][i % 4]) * x_scale * scale[i];
+                    if (!known) v[i] = 0.0f;
+                }
+                const int64_t o = (t.row + r) * a.N + t.channel + c;
+                if (a.vec) {
+                    if (a.out_f32) F32::store<V>(a.out, o, v);
+                    else
+                        Bf16::store<V>(a.out, o, v);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < V; ++i) {
+                        if (t.channel + c + i >= a.N) continue;
+                        const float one[1] = {v[i]};
+                        if (a.out_f32) F32::store<1>(a.out, o + i, one);
+                        else
+                            Bf16::store<1>(a.out, o + i, one);
+                    }
+                }
+            }
+        }
+    }
+};
+
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(N) : "memory");
+}
+
+// 16 (4) bytes a lane from memory to consecutive LDS addresses, past the registers.
+// The builtin for this makes the compiler wait for all of them before the next
+// read of LDS (a large matrix: 1230 against 1010 us); here wait_loads and the
+// barrier behind it order them.  No register is written, so there is no output
+// that the compiler could take as ready; m0's write needs one wait state.
+__device__ __forceinline__ uint32_t lds_address(const void* lds) {
+    return static_cast<uint32_t>(reinterpret_cast<uintptr_t>((const __attribute__((address_space(3))) void*)lds));
+}
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"  // that m0 is named as overwritten
+__device__ __forceinline__ void load16_to_lds(const void* p, const void* lds) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds_address(lds)), "v"(p)
+                 : "memory", "m0");
+}
+__device__ __forceinline__ void load4_to_lds(const void* p, const void* lds) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(lds_address(lds)), "v"(p)
+                 : "memory", "m0");
+}
+#pragma clang diagnostic pop
+
+// Rows of whole, aligned 16-byte chunks.  The workgroup stays and takes one tile
+// after another; its loads run ahead of the products, SX - 1 steps those of x and
+// SW - 1 those of w, across the tiles' ends, so that neither the start of a tile
+// nor its stores leave the matrix units or the memory idle.  A tile's scales are
+// loaded with its first steps.  SX is SW, or 2 where LDS has no room for more: x
+// comes from the L2 mostly, w from memory.
+template <int BM, int BN, int BK, int SX, int SW, int WM, int WN>
+__global__ __launch_bounds__(WM* WN* kWave) void expert_matmul_int8_kernel(MatmulArgs a) {
+    using Y = Layout<BM, BN, BK, WM, WN>;
+    constexpr int kWaves = Y::kWaves, kThreads = kWaves * kWave;
+    constexpr int kX = (Y::kXLoads + kWaves - 1) / kWaves, kW = Y::kWLoads / kWaves;  // loads of a wave and step
+    constexpr bool kEven = Y::kXLoads % kWaves == 0;  // else the first waves have one more of x
+    static_assert(SX == SW ? SW == 2 || kEven : SX == 2 && SW == 3, "what the waits count");
+    // the loads that may be under way still when a step's have to be there: those
+    // of later steps, if they come after the step's own
+    constexpr int kLater = SX == SW ? (SW - 2) * (kX + kW) : kW;
+    static_assert(BM <= kThreads && BN % kWave == 0, "a thread for each row's scale, whole waves for the channels'");
+    constexpr int kScales = (BM + kWave - 1) / kWave * kWave;  // whole waves load them
+    __shared__ __attribute__((aligned(1024))) uint8_t x_stages[SX][BM * BK], w_stages[SW][BN * BK];
+    // of each tile that the loads may be ahead
+    __shared__ float x_scale[SW][kScales], w_scale[SW][BN];
+    __shared__ uint8_t known[SW][BM];
+    __shared__ Tile tiles_ahead[SW];
+
+    const Tiles<BM, BN> tiles(a);
+    // workgroups go to the dies in turn; a die's take one run of tiles by turns
+    const int die = blockIdx.x % kXcds, stride = gridDim.x / kXcds;
+    int64_t id = tiles.start_of(die, kXcds) + blockIdx.x / kXcds;
+    const int64_t end = tiles.start_of(die + 1, kXcds);
+    if (id >= end) return;
+    const int lane = threadIdx.x % kWave, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const int steps = (a.K + BK - 1) / BK;
+    int64_t left = (end - id + stride - 1) / stride * steps;  // steps to multiply
+    const int line_row = lane / Y::kChunks, line_chunk = lane % Y::kChunks;  // the lane's place in a load
+
+    // The loads' side.  `next` is the tile that w comes to next, `after` the one
+    // that x does; a tile's row tokens are read one step before x needs them.
+    Tile next = tiles.find(id), after = next;
+    int token[kX], my_token = 0;
+    const uint8_t *x_src[kX], *w_src[kW];
+    int x_step = 0, w_step = 0, x_slot = 0, w_slot = 0, x_stage = 0, w_stage = 0;
+    int x_tiles = 0, w_tiles = 0;  // begun
+    bool more = true;
+    auto read_tokens = [&](const Tile& t) {
+        after = t;
+#pragma unroll
+        for (int j = 0; j < kX; ++j) {
+            // rows past the tile's read its last one again and are not stored
+            const int64_t row = t.row + min((wave + j * kWaves) * Y::kRowsPerLoad + line_row, t.rows - 1);
+            token[j] = a.row_token != nullptr ? a.row_token[row] : static_cast<int>(row);
+        }
+        const int64_t row = t.row + min(static_cast<int>(threadIdx.x), t.rows - 1);
+        my_token = a.row_token != nullptr ? a.row_token[row] : static_cast<int>(row);
+    };
+    auto load_x = [&]() {
+        if (x_step == 0) {
+            if (x_tiles == w_tiles + (SX == SW && more)) return;  // no tile left
+            ++x_tiles;
+#pragma unroll
+            for (int j = 0; j < kX; ++j) {
+                const int r = (wave + j * kWaves) * Y::kRowsPerLoad + line_row;
+                // a row without a token is stored as zeros, whatever it reads
+                const int x = token[j] >= 0 && token[j] < a.x_rows ? token[j] : 0;
+                x_src[j] = a.x + static_cast<int64_t>(x) * a.K + (line_chunk ^ Y::x_swizzle(r)) * 16;
+            }
+            const bool has = my_token >= 0 && my_token < a.x_rows;
+            if (threadIdx.x < BM) known[x_slot][threadIdx.x] = has;
+            if (threadIdx.x == 0) tiles_ahead[x_slot] = after;
+            if (wave * kWave < BM)
+                load4_to_lds(has ? static_cast<const void*>(a.x_sf + my_token) : &kZeroChunk,
+                             &x_scale[x_slot][wave * kWave]);
+        }
+#pragma unroll
+        for (int j = 0; j < kX; ++j) {
+            if (!kEven && wave + j * kWaves >= Y::kXLoads) continue;
+            const uint8_t* p = x_src[j];
+            if ((x_step + 1) * BK > a.K) {  // past the end of k: zeros
+                const int r = (wave + j * kWaves) * Y::kRowsPerLoad + line_row;
+                if (x_step * BK + (line_chunk ^ Y::x_swizzle(r)) * 16 >= a.K)
+                    p = reinterpret_cast<const uint8_t*>(&kZeroChunk);
+            }
+            load16_to_lds(p, x_stages[x_stage] + (wave + j * kWaves) * 1024);
+            x_src[j] += BK;
+        }
+        x_stage = x_stage + 1 == SX ? 0 : x_stage + 1;
+        if (++x_step == steps) {
+            x_step = 0;
+            x_slot = x_slot + 1 == SW ? 0 : x_slot + 1;
+        }
+    };
+    auto load_w = [&]() {
+        if (w_step == 0) {
+            ++w_tiles;
+            const int64_t first = static_cast<int64_t>(next.expert) * a.N;
+#pragma unroll
+            for (int j = 0; j < kW; ++j) {
+                const int r = (wave + j * kWaves) * Y::kRowsPerLoad + line_row;
+                w_src[j] = a.w + (first + min(next.channel + r, a.N - 1)) * a.K + (line_chunk ^ Y::w_swizzle(r)) * 16;
+            }
+#pragma unroll
+            for (int i = 0; i < (BN + kThreads - 1) / kThreads; ++i) {
+                const int c = i * kThreads + wave * kWave;
+                if (c < BN) load4_to_lds(a.w_sf + first + min(next.channel + c + lane, a.N - 1), &w_scale[w_slot][c]);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < kW; ++j) {
+            const uint8_t* p = w_src[j];
+            if ((w_step + 1) * BK > a.K) {
+                const int r = (wave + j * kWaves) * Y::kRowsPerLoad + line_row;
+                if (w_step * BK + (line_chunk ^ Y::w_swizzle(r)) * 16 >= a.K)
+                    p = reinterpret_cast<const uint8_t*>(&kZeroChunk);
+            }
+            load16_to_lds(p, w_stages[w_stage] + (wave + j * kWaves) * 1024);
+            w_src[j] += BK;
+        }
+        if (SX != SW && w_step == 0) read_tokens(next);  // x comes to this tile one step later
+        w_stage = w_stage + 1 == SW ? 0 : w_stage + 1;
+        if (++w_step == steps) {
+            w_step = 0;
+            w_slot = w_slot + 1 == SW ? 0 : w_slot + 1;
+            id += stride;
+            more = id < end;
+            if (more) {
+                next = tiles.find(id);
+                if (SX == SW) read_tokens(next);
+            }
+        }
+    };
+
+    if (SX == SW) read_tokens(next);
+    int ahead = 0;  // steps of w loaded or loading
+    for (int i = 0; i < SW - 1; ++i) {
+        if (i >= SW - SX) load_x();
+        if (more) {
+            load_w();
+            ++ahead;
+        }
+    }
+
+    const int wm = wave / WN, wn = wave % WN;
+    typename Y::Sums acc;
+    int xs = 0, ws = 0, slot = 0, step = 0, used = 0;
+    for (; left > 0; --left) {
+        if (ahead == SW - 1) wait_loads<kLater>();
+        else
+            wait_loads<0>();
+        // every wave's part of this step is there, and every wave is done with the step before it
+        __builtin_amdgcn_s_barrier();
+        if (step == 0) {
+            used = Y::used_blocks(__builtin_amdgcn_readfirstlane(tiles_ahead[slot].rows), wm);
+#pragma unroll
+            for (int m = 0; m < Y::TM; ++m)
+#pragma unroll
+                for (int n = 0; n < Y::TN; ++n) acc[m][n] = i32x4_t{0, 0, 0, 0};
+        }
+        --ahead;
+        load_x();
+        if (more) {
+            load_w();
+            ++ahead;
+        }
+        Y::multiply(x_stages[xs], w_stages[ws], used, wm, wn, lane, acc);
+        xs = xs + 1 == SX ? 0 : xs + 1;
+        ws = ws + 1 == SW ? 0 : ws + 1;
+        if (++step < steps) continue;
+        step = 0;
+        const Tile t = tiles_ahead[slot];
+        Y::store(
+            a, t, wm, wn, lane, acc,
+            [&](int r, bool& has) {
+                has = known[slot][r];
+                return x_scale[slot][r];
+            },
+            [&](int c) { return w_scale[slot][c]; });
+        slot = slot + 1 == SW ? 0 : slot + 1;
+    }
 }
 
 // Sixteen bytes at any address; past `left` bytes zeros.
@@ -145,183 +510,127 @@ __device__ __forceinline__ u32x4_t load_any(const uint8_t* p, int left) {
     return v;
 }
 
-// WM x WN waves, each BM / WM rows and BN / WN channels.  DIRECT: rows are 16-byte
-// aligned and go straight to LDS; else through registers, one step ahead.
-template <int BM, int BN, int BK, int STAGES, int WM, int WN, bool DIRECT>
-__global__ __launch_bounds__(WM* WN* kWave) void expert_matmul_int8_kernel(MatmulArgs a) {
-    constexpr int kWaves = WM * WN;
-    constexpr int kChunks = BK / 16;                     // of a row
-    constexpr int kRowsPerLoad = kWave / kChunks;        // rows that a wave's load covers
-    constexpr int kLoads = (BM + BN) / kRowsPerLoad / kWaves;  // of a wave and step
-    constexpr int kStage = (BM + BN) * BK;
-    constexpr int TM = BM / WM / 16, TN = BN / WN / 16;
-    static_assert((BM + BN) % (kRowsPerLoad * kWaves) == 0 && BM % (16 * WM) == 0 && BN % (16 * WN) == 0, "tile");
-    static_assert(BM % kRowsPerLoad == 0, "a load lies in x or in w");
-    static_assert(DIRECT || STAGES == 2, "two stages through registers");
-    __shared__ __attribute__((aligned(1024))) uint8_t lds[STAGES][kStage];
-
-    Tile t;
-    if (!find_tile<BM, BN>(a, t)) return;
+// Rows of any length at any address: the next step's chunks are in registers
+// while this one's are multiplied.
+template <int BM, int BN, int BK, int WM, int WN>
+__global__ __launch_bounds__(WM* WN* kWave) void expert_matmul_int8_odd_kernel(MatmulArgs a) {
+    using Y = Layout<BM, BN, BK, WM, WN>;
+    constexpr int kLoads = (Y::kXLoads + Y::kWLoads) / Y::kWaves;
+    static_assert(Y::kXLoads % Y::kWaves == 0, "a load lies in x or in w");
+    __shared__ __attribute__((aligned(1024))) uint8_t stages[2][(BM + BN) * BK];
+    const Tiles<BM, BN> tiles(a);
+    const int die = blockIdx.x % kXcds, stride = gridDim.x / kXcds;
     const int lane = threadIdx.x % kWave, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-
-    // this lane's chunk of each of its wave's loads
-    const uint8_t* src[kLoads];
-    int at[kLoads];  // its k within a step
-#pragma unroll
-    for (int j = 0; j < kLoads; ++j) {
-        const int r = (wave + j * kWaves) * kRowsPerLoad + lane / kChunks;  // row of the stage
-        const int c = swizzle<BK>(r, lane % kChunks);
-        int64_t row;
-        if (r < BM) {  // x: rows past the tile's read its last one again and are not stored
-            row = t.row + min(r, t.rows - 1);
-            if (a.row_token != nullptr) row = a.row_token[row];
-            if (row < 0 || row >= a.x_rows) row = 0;  // stored as zeros
-            src[j] = a.x + row * a.K;
-        } else {
-            row = static_cast<int64_t>(t.expert) * a.N + min(t.channel + r - BM, a.N - 1);
-            src[j] = a.w + row * a.K;
-        }
-        at[j] = c * 16;
-        src[j] += at[j];
-    }
+    const int wm = wave / WN, wn = wave % WN;
     const int steps = (a.K + BK - 1) / BK;
-    auto issue = [&](int step, int stage) {
-        const bool last = (step + 1) * BK > a.K;
+    const int64_t end = tiles.start_of(die + 1, kXcds);
+    for (int64_t id = tiles.start_of(die, kXcds) + blockIdx.x / kXcds; id < end; id += stride) {
+        const Tile t = tiles.find(id);
+        const uint8_t* src[kLoads];
+        int left[kLoads];  // bytes of the row from this lane's chunk on
 #pragma unroll
         for (int j = 0; j < kLoads; ++j) {
-            const uint8_t* p = src[j] + static_cast<int64_t>(step) * BK;
-            if (last && step * BK + at[j] >= a.K) p = reinterpret_cast<const uint8_t*>(&kZeroChunk);
-            __builtin_amdgcn_global_load_lds(
-                reinterpret_cast<const __attribute__((address_space(1))) void*>(reinterpret_cast<uintptr_t>(p)),
-                (__attribute__((address_space(3))) void*)(lds[stage] + (wave + j * kWaves) * 1024), 16, 0, 0);
+            const int r = (wave + j * Y::kWaves) * Y::kRowsPerLoad + lane / Y::kChunks;
+            const int place = lane % Y::kChunks, c = place ^ (r < BM ? Y::x_swizzle(r) : Y::w_swizzle(r - BM));
+            if (r < BM) {
+                int64_t row = t.row + min(r, t.rows - 1);
+                if (a.row_token != nullptr) row = a.row_token[row];
+                src[j] = a.x + (row >= 0 && row < a.x_rows ? row : 0) * a.K + c * 16;
+            } else {
+                src[j] = a.w + (static_cast<int64_t>(t.expert) * a.N + min(t.channel + r - BM, a.N - 1)) * a.K + c * 16;
+            }
+            left[j] = a.K - c * 16;
         }
-    };
-    u32x4_t held[DIRECT ? 1 : kLoads];
-    auto fetch = [&](int step) {
+        u32x4_t held[kLoads];
+        auto fetch = [&]() {
 #pragma unroll
-        for (int j = 0; j < kLoads; ++j)
-            held[j] = load_any(src[j] + static_cast<int64_t>(step) * BK, a.K - step * BK - at[j]);
-    };
-
-    const int wm = wave / WN, wn = wave % WN;
-    const int x_row = wm * (BM / WM) + lane % 16, w_row = BM + wn * (BN / WN) + lane % 16;
-    const bool busy = wm * (BM / WM) < t.rows;  // a wave whose rows are all past the tile's has nothing to sum
-    i32x4_t acc[TM][TN];
+            for (int j = 0; j < kLoads; ++j) {
+                held[j] = load_any(src[j], left[j]);
+                src[j] += BK;
+                left[j] -= BK;
+            }
+        };
+        const int used = Y::used_blocks(t.rows, wm);
+        typename Y::Sums acc;
 #pragma unroll
-    for (int m = 0; m < TM; ++m)
+        for (int m = 0; m < Y::TM; ++m)
 #pragma unroll
-        for (int n = 0; n < TN; ++n) acc[m][n] = i32x4_t{0, 0, 0, 0};
-    auto multiply = [&](int stage) {
-        const uint8_t* s = lds[stage];
-#pragma unroll
-        for (int k = 0; k < BK / 64; ++k) {
-            i32x4_t xf[TM], wf[TN];
-            const int c = k * 4 + lane / 16;
-#pragma unroll
-            for (int n = 0; n < TN; ++n)
-                wf[n] = *reinterpret_cast<const i32x4_t*>(s + (w_row + n * 16) * BK + swizzle<BK>(w_row, c) * 16);
-#pragma unroll
-            for (int m = 0; m < TM; ++m)
-                xf[m] = *reinterpret_cast<const i32x4_t*>(s + (x_row + m * 16) * BK + swizzle<BK>(x_row, c) * 16);
-#pragma unroll
-            for (int m = 0; m < TM; ++m)
-#pragma unroll
-                for (int n = 0; n < TN; ++n)
-                    acc[m][n] = __builtin_amdgcn_mfma_i32_16x16x64_i8(wf[n], xf[m], acc[m][n], 0, 0, 0);
-        }
-    };
-
-    if constexpr (DIRECT) {
-#pragma unroll
-        for (int i = 0; i < STAGES - 1; ++i)
-            if (i < steps) issue(i, i);
-        int stage = 0;
+            for (int n = 0; n < Y::TN; ++n) acc[m][n] = i32x4_t{0, 0, 0, 0};
+        __syncthreads();  // every wave is done with the tile before
+        fetch();
         for (int i = 0; i < steps; ++i) {
-            if (i + STAGES - 2 < steps) wait_loads<(STAGES - 2) * kLoads>();
-            else
-                wait_loads<0>();
-            // every wave's part of this step is there, and every wave is done with the step before it
-            __builtin_amdgcn_s_barrier();
-            if (i + STAGES - 1 < steps) issue(i + STAGES - 1, stage == 0 ? STAGES - 1 : stage - 1);
-            if (busy) multiply(stage);
-            stage = stage + 1 == STAGES ? 0 : stage + 1;
-        }
-    } else {
-        fetch(0);
-        for (int i = 0; i < steps; ++i) {
-            uint8_t* s = lds[i & 1];
+            uint8_t* s = stages[i & 1];
 #pragma unroll
             for (int j = 0; j < kLoads; ++j)
-                *reinterpret_cast<u32x4_t*>(s + (wave + j * kWaves) * 1024 + lane * 16) = held[j];
-            if (i + 1 < steps) fetch(i + 1);
+                *reinterpret_cast<u32x4_t*>(s + (wave + j * Y::kWaves) * 1024 + lane * 16) = held[j];
+            if (i + 1 < steps) fetch();
             __syncthreads();
-            if (busy) multiply(i & 1);
+            Y::multiply(s, s + BM * BK, used, wm, wn, lane, acc);
         }
-    }
-    if (!busy) return;
-
-    // lane l holds four channels, 4 (l / 16) on, of row l % 16 of each 16 x 16 product
-#pragma unroll
-    for (int m = 0; m < TM; ++m) {
-        const int r = wm * (BM / WM) + m * 16 + lane % 16;
-        if (r >= t.rows) continue;
-        const int64_t row = t.row + r;
-        int64_t from = row;
-        if (a.row_token != nullptr) from = a.row_token[row];
-        const bool known = from >= 0 && from < a.x_rows;
-        const float xs = known ? a.x_sf[from] : 0.0f;
-#pragma unroll
-        for (int n = 0; n < TN; ++n) {
-            const int ch = t.channel + wn * (BN / WN) + n * 16 + lane / 16 * 4;
-            const float* ws = a.w_sf + static_cast<int64_t>(t.expert) * a.N + ch;
-            const int64_t o = row * a.N + ch;
-            float v[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                v[i] = known && ch + i < a.N ? static_cast<float>(acc[m][n][i]) * xs * ws[i] : 0.0f;
-            if (a.vec4) {
-                if (ch >= a.N) continue;
-                if (a.out_f32) F32::store<4>(a.out, o, v);
-                else
-                    Bf16::store<4>(a.out, o, v);
-            } else {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    if (ch + i >= a.N) continue;
-                    float one[1] = {v[i]};
-                    if (a.out_f32) F32::store<1>(a.out, o + i, one);
-                    else
-                        Bf16::store<1>(a.out, o + i, one);
-                }
-            }
-        }
+        Y::store(
+            a, t, wm, wn, lane, acc,
+            [&](int r, bool& has) {
+                int64_t row = t.row + r;
+                if (a.row_token != nullptr) row = a.row_token[row];
+                has = row >= 0 && row < a.x_rows;
+                return has ? a.x_sf[row] : 0.0f;
+            },
+            [&](int c) { return t.channel + c < a.N ? a.w_sf[static_cast<int64_t>(t.expert) * a.N + t.channel + c] : 0.0f; });
     }
 }
 
-template <int BM, int BN, int BK, int STAGES, int WM, int WN, bool DIRECT>
+// The most tiles that there can be: an expert adds at most one that is not full.
+int64_t most_tiles(const MatmulArgs& a, int bm) {
+    const int64_t experts = a.E < a.num_rows ? a.E : a.num_rows;
+    const int64_t slots = a.num_rows / bm + experts;
+    return (slots < a.num_rows ? slots : a.num_rows) * a.n_tiles;
+}
+unsigned whole_dies(int64_t blocks) { return static_cast<unsigned>((blocks + kXcds - 1) / kXcds * kXcds); }
+
+// PER_CU workgroups fit a compute unit's LDS.
+template <int BM, int BN, int BK, int SX, int SW, int WM, int WN, int PER_CU>
 hipError_t launch_tiles(MatmulArgs a, hipStream_t stream) {
     a.n_tiles = (a.N + BN - 1) / BN;
-    // an expert adds at most one partly filled tile; the kernel counts the tiles that there are
-    const int64_t experts = a.E < a.num_rows ? a.E : a.num_rows;
-    int64_t slots = a.num_rows / BM + experts;
-    if (slots > a.num_rows) slots = a.num_rows;
-    const int64_t blocks = (slots * a.n_tiles + kXcds - 1) / kXcds * kXcds;
-    hipLaunchKernelGGL((expert_matmul_int8_kernel<BM, BN, BK, STAGES, WM, WN, DIRECT>),
-                       dim3(static_cast<unsigned>(blocks)), dim3(WM * WN * kWave), 0, stream, a);
+    const int64_t places = static_cast<int64_t>(device_cu_count()) * PER_CU, tiles = most_tiles(a, BM);
+    hipLaunchKernelGGL((expert_matmul_int8_kernel<BM, BN, BK, SX, SW, WM, WN>),
+                       dim3(whole_dies(tiles < places ? tiles : places)), dim3(WM * WN * kWave), 0, stream, a);
     return hipGetLastError();
 }
 
-template <bool DIRECT>
-hipError_t launch_matmul(const MatmulArgs& a, hipStream_t stream) {
-    const int64_t mean = a.num_rows / a.E;
-    if constexpr (!DIRECT) {
-        if (mean <= 16) return launch_tiles<16, 64, 256, 2, 1, 4, false>(a, stream);
-        return launch_tiles<64, 64, 128, 2, 2, 2, false>(a, stream);
-    } else {
-        if (mean <= 16) return launch_tiles<16, 64, 256, 4, 1, 4, true>(a, stream);
-        if (mean <= 64) return launch_tiles<64, 64, 128, 4, 1, 4, true>(a, stream);
-        return launch_tiles<256, 256, 128, 2, 2, 4, true>(a, stream);
+template <int BM, int BN, int BK, int WM, int WN>
+hipError_t launch_odd(MatmulArgs a, hipStream_t stream) {
+    a.n_tiles = (a.N + BN - 1) / BN;
+    hipLaunchKernelGGL((expert_matmul_int8_odd_kernel<BM, BN, BK, WM, WN>), dim3(whole_dies(most_tiles(a, BM))),
+                       dim3(WM * WN * kWave), 0, stream, a);
+    return hipGetLastError();
+}
+
+// The form for a batch.  Large tiles read x and w less often and keep the matrix
+// units busier; small ones fill the chip where there are few, and read no more
+// rows than there are.  The host knows the experts' mean row count, not each one's.
+hipError_t launch_matmul(const MatmulArgs& a, bool direct, hipStream_t stream) {
+    const int64_t busy = a.E < a.num_rows ? a.E : a.num_rows, mean = (a.num_rows + busy - 1) / busy;
+    auto tiles = [&](int64_t bm, int64_t bn) { return busy * ((mean + bm - 1) / bm) * ((a.N + bn - 1) / bn); };
+    if (!direct) {
+        if (mean <= 16) return launch_odd<16, 64, 256, 1, 4>(a, stream);
+        return launch_odd<64, 64, 128, 2, 2>(a, stream);
     }
+    const int64_t cus = device_cu_count();
+    // one tile holds most experts' rows (32 experts, 7168 -> 4096, 128 rows: 98 us; 108 us in tiles of 32 x 128), or
+    // the places of two workgroups a compute unit are not all taken (256 rows of one matrix, 4096 -> 2048: 15.4
+    // against 21.2 us; 1024 rows, 1024 -> 1024, two for each place: 11.5 against 8.9 us)
+    if (mean <= 8 || tiles(16, 64) <= 2 * cus) return launch_tiles<16, 64, 256, 3, 3, 1, 4, 2>(a, stream);
+    // 32 experts, 7168 -> 4096, 1024 rows an expert: 1060 against 1120 us in the next; 512: 635 against 596 us
+    if (mean > 768 && tiles(256, 256) >= 2 * cus) return launch_tiles<256, 256, 128, 2, 2, 2, 4, 1>(a, stream);
+    // the same, 512 rows: 596 against 662 us in the next; 64 rows: 224 against 198 us
+    if (mean > 160 && tiles(192, 256) >= cus) return launch_tiles<192, 256, 128, 2, 3, 2, 4, 1>(a, stream);
+    // the same, 64 rows: 198 against 218 us in the next; 2048 rows of one matrix, 2048 -> 2048, 128 tiles of this
+    // size: 23.1 against 20.6 us
+    if (tiles(128, 256) >= cus) return launch_tiles<128, 256, 128, 3, 3, 2, 4, 1>(a, stream);
+    // 4096 rows of one matrix, 7168 -> 512: 38 against 40 us in the last; 1024 rows, 1024 -> 1024, 128 tiles of this
+    // size: 9.9 against 8.9 us
+    if (tiles(64, 128) >= cus) return launch_tiles<64, 128, 128, 3, 3, 2, 4, 2>(a, stream);
+    return launch_tiles<32, 128, 128, 3, 3, 1, 4, 2>(a, stream);
 }
 
 }  // namespace
@@ -364,7 +673,7 @@ extern "C" moe_status moe_expert_matmul_int8(const int8_t* x, const float* x_sf,
     a.w_sf = w_sf;
     a.out = out;
     a.out_f32 = out_dtype == MOE_DTYPE_F32;
-    a.vec4 = out_width % 4 == 0 && aligned(out, 4 * size);
+    a.vec = out_width % 8 == 0 && aligned(out, 16);
     const bool direct = inner % 16 == 0 && aligned(a.x, 16) && aligned(w, 16);
-    return hip_status(direct ? launch_matmul<true>(a, stream) : launch_matmul<false>(a, stream));
+    return hip_status(launch_matmul(a, direct, stream));
 }
