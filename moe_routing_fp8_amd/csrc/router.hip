@@ -5,18 +5,21 @@
 // topk_groups groups with the largest group scores, and their weights are
 //   w_k = scale * s_k   or, renormalised,   scale * s_k / sum_j s_j.
 //
-// Forward, one launch: a row lies over 16 lanes (64 above 256 experts), expert
-// e in slot e / L of lane e % L.  Every lane sorts its keys once, then each of
-// the K rounds takes the maximum over the lanes' heads, four rows of a wave
-// side by side.
+// Forward, one launch: a row lies over 16 lanes (64 above 256 experts), P
+// consecutive experts a lane.  Every lane sorts its keys once, then each of the K
+// rounds takes the maximum over the lanes' heads, four rows of a wave side by
+// side.  Where a group is made of whole lanes, as 8 groups of 32 are, its best
+// experts are the lanes' first ones.
 //
-// The order is that of the values in 64 bits, while the keys hold 28 bits of
-// an fp32 value and the slot (larger keys are lower slots, so equal values go
-// to the lowest expert without another comparison).  Neighbours of the
-// resulting order, and the last one taken and the best one left, are compared
-// once at the end: only a row where two of them lie closer than the keys'
-// error, without being equal bit by bit in what they are made of, is ordered
-// again, in 64 bits, by its whole wave.
+// The order is that of the values in 64 bits, while a key holds 28 bits of an
+// fp32 value (26 above 256 experts) and the slot, or in a round's maximum the
+// lane: larger keys are lower ones, so equal values go to the lowest expert.
+// Neighbours of the resulting order, and the last expert taken and the best one
+// left, are compared once at the end.  Only a row where two of them lie closer
+// than the keys' error, without being equal bit by bit in what they are made of,
+// is ordered again, about one of a hundred: the experts taken and the one left
+// that is near them by their values in 64 bits, a lane each; or, where more than
+// one is near or groups are, all of them, by the whole wave.
 //
 // Backward, one launch: the chosen experts' derivatives are laid into a row of
 // zeros in LDS, from where the row is written in whole vectors; softmax
@@ -36,9 +39,9 @@ namespace {
 
 constexpr int kWaves = 4;            // of a workgroup
 constexpr int kNarrowExperts = 256;  // rows of up to this many experts lie over 16 lanes
-constexpr int kMaxGroups = 64;       // MOE_ROUTER_MAX_GROUPS
-constexpr uint32_t kSlotMask = 15;   // the key's bits that hold the slot
-constexpr uint32_t kNone = 0;        // the key of an expert that cannot be taken: below every value's
+constexpr int kMaxGroups = MOE_ROUTER_MAX_GROUPS;
+constexpr int kDppRowShl1 = 0x101;  // lane i + 1 of the same row (lane 15 of a row reads 0)
+constexpr uint32_t kNone = 0x007FFFFF;  // keys up to -inf's: no expert
 
 struct RouterArgs {
     const void* logits;
@@ -46,7 +49,8 @@ struct RouterArgs {
     int E, K, sigmoid;
     const float* bias;
     int groups, topk_groups, group_size, top2;
-    int lanes_per_group;  // lanes that share the scan of one group
+    int lanes_per_group;   // of whole lanes, if a group is; else lanes that share its scan
+    int whole_lanes;
     uint32_t group_magic;  // e / group_size == umulhi(e, group_magic) (group_size > 1)
     int renormalize;
     float scale;
@@ -59,16 +63,10 @@ struct RouterArgs {
 // largest finite value.
 __device__ __forceinline__ float clean(float z) { return z != z ? -INFINITY : fminf(z, FLT_MAX); }
 
-__device__ __forceinline__ bool takeable(float z, const float* bias, int e) {
-    return z > -INFINITY && (bias == nullptr || bias[e] > -INFINITY);
-}
-
-// sigmoid(z) to 4 ulp: the exponential of an exact argument to 1.5 ulp, a sum,
-// the hardware reciprocal and a product.
+// sigmoid(z) to order by: 3 ulp, and the exponent's rounding, |z| 2^-23 of an
+// exponential that counts s (1 - s): below 2^-22 in all.
 __device__ __forceinline__ float sigmoid_key(float z) {
-    const float e = exp_nonpos_exact(-fabsf(z));
-    const float r = __builtin_amdgcn_rcpf(1.0f + e);
-    return z < 0.0f ? e * r : r;
+    return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(z * -1.44269504088896340736f));
 }
 
 template <int L>
@@ -100,11 +98,14 @@ __device__ __forceinline__ void sort_desc(uint32_t (&key)[P]) {
     }
 }
 
-__device__ __forceinline__ uint32_t order_key(float v) { return topk::score_key(v); }
 __device__ __forceinline__ float key_value(uint32_t k) {
     return __uint_as_float((k & 0x80000000u) ? (k ^ 0x80000000u) : ~k);
 }
-
+// -0 becomes +0; no NaN comes here.
+__device__ __forceinline__ uint32_t order_key(float v) {
+    const uint32_t u = __float_as_uint(v + 0.0f);
+    return u ^ (static_cast<uint32_t>(static_cast<int32_t>(u) >> 31) | 0x80000000u);
+}
 __device__ __forceinline__ uint64_t order_key64(double v) {
     const uint64_t u = static_cast<uint64_t>(__double_as_longlong(v + 0.0));
     return (u >> 63) ? ~u : (u | 0x8000000000000000ull);
@@ -118,106 +119,102 @@ __device__ __forceinline__ void lds_handoff() {
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
-// LDS of a wave.  `value` holds the scores that the groups are judged by: fp32
-// [rows][E], or 64-bit [E] while a row is ordered exactly.
+// LDS of a wave.  `value` holds what groups that are not whole lanes are judged
+// by, fp32 [rows][E], or the 64-bit values [E] of a row that is ordered exactly.
 template <int L, int P>
 struct WaveLds {
     static constexpr int kRows = kWave / L;
-    double value[L * P > kNarrowExperts ? L * P : kRows * L * P / 2];
-    double group[kMaxGroups];
-    int taken[kRows][kMaxGroups];
-    int winner[kRows][16];
+    static constexpr int kValues = kRows == 1 ? L * P : kRows * L * P / 2;
+    double value[kValues];
+    union {
+        float best[kRows][2 * L > kMaxGroups ? 2 * L : kMaxGroups];  // of a lane or a group; then whether it is taken
+        int winner[kRows][16];                                       // once the groups are chosen
+    };
 };
 
-// The order of one row in 64 bits, by the whole wave: expert e is value e / 64
-// of lane e % 64.
+template <typename T>
+__device__ __forceinline__ float logit(const RouterArgs& a, int64_t i) {
+    float f[1];
+    T::template load<1>(a.logits, i, f);
+    return clean(f[0]);
+}
+
+// One row in 64 bits, by the whole wave, through LDS.  Rare, so these take few
+// registers; but what they take, the last wave of a launch adds to its time, most
+// of it for code that no other wave has fetched.
+//
+// The values that experts, or with `groups` groups, are judged by: -inf for an
+// expert that cannot be taken.
 template <typename T, int Q>
-__device__ __forceinline__ void exact_row(const RouterArgs& a, int64_t t, double* value, double* group, int* taken,
-                                       int* winner, int lane) {
-    float z[Q];
-    double c[Q];
-    float top = -INFINITY;
-#pragma unroll
-    for (int j = 0; j < Q; ++j) {
-        const int e = j * kWave + lane;
-        float f[1] = {-INFINITY};
-        if (e < a.E) T::template load<1>(a.logits, t * a.row_stride + e, f);
-        z[j] = clean(f[0]);
-        top = fmaxf(top, z[j]);
-    }
-    if (!a.sigmoid) {
-        top = group_max_f32<kWave>(top);
-        double sum = 0.0;
-#pragma unroll
-        for (int j = 0; j < Q; ++j) {
-            c[j] = z[j] > -INFINITY ? exp(static_cast<double>(z[j]) - static_cast<double>(top)) : 0.0;
-            sum += c[j];
-        }
-        for (int o = 1; o < kWave; o *= 2) sum += __shfl_xor(sum, o);
-#pragma unroll
-        for (int j = 0; j < Q; ++j) c[j] /= sum;
-    } else {
-#pragma unroll
-        for (int j = 0; j < Q; ++j) c[j] = 1.0 / (1.0 + exp(-static_cast<double>(z[j])));
-    }
+__device__ __forceinline__ void exact_values(const RouterArgs& a, int64_t t, double* value, bool scores, int lane) {
+    const int64_t base = t * a.row_stride;
     const bool by_value = a.bias != nullptr;
+    float high = -INFINITY;
 #pragma unroll
     for (int j = 0; j < Q; ++j) {
         const int e = j * kWave + lane;
-        const bool open = e < a.E && takeable(z[j], a.bias, e);
-        if (by_value && open) c[j] += static_cast<double>(fminf(a.bias[e], FLT_MAX));
-        if (!open) c[j] = -INFINITY;
-        if (!by_value && !a.top2) c[j] = open ? static_cast<double>(z[j]) : -INFINITY;
+        if (e >= a.E) continue;
+        const float z = logit<T>(a, base + e);
+        high = fmaxf(high, z);
+        value[e] = by_value && !(a.bias[e] > -INFINITY) ? -INFINITY : static_cast<double>(z);
     }
-    if (a.groups > 1) {
-#pragma unroll
-        for (int j = 0; j < Q; ++j) {
-            const int e = j * kWave + lane;
-            if (e < a.E) value[e] = c[j];
-        }
-        lds_handoff();
-        if (lane < a.groups) {
-            double b1 = -INFINITY, b2 = -INFINITY;
-            for (int i = 0; i < a.group_size; ++i) {
-                const double v = value[lane * a.group_size + i];
-                b2 = fmax(b2, fmin(b1, v));
-                b1 = fmax(b1, v);
+    if (scores) {
+        double top = 0.0, sum = 1.0;
+        if (!a.sigmoid) {
+            top = static_cast<double>(group_max_f32<kWave>(high));
+            sum = 0.0;
+#pragma unroll 1
+            for (int e = lane; e < a.E; e += kWave) {
+                // an expert that only its bias takes out has its part in the sum
+                const double z = by_value ? static_cast<double>(logit<T>(a, base + e)) : value[e];
+                if (z > -INFINITY) sum += exp(z - top);
             }
-            group[lane] = a.top2 ? b1 + b2 : b1;
+            for (int o = 1; o < kWave; o *= 2) sum += __shfl_xor(sum, o);
         }
-        lds_handoff();
-        if (lane < a.groups) {
-            const double mine = group[lane];
-            int rank = 0;
-            for (int h = 0; h < a.groups; ++h) {
-                const double o = group[h];
-                rank += o > mine || (o == mine && h < lane);
-            }
-            taken[lane] = rank < a.topk_groups;
+#pragma unroll 1
+        for (int e = lane; e < a.E; e += kWave) {
+            const double z = value[e];
+            if (!(z > -INFINITY)) continue;
+            const double x = exp(a.sigmoid ? -z : z - top);
+            double c = a.sigmoid ? 1.0 / (1.0 + x) : x / sum;
+            if (by_value) c += static_cast<double>(fminf(a.bias[e], FLT_MAX));
+            value[e] = c;
         }
-        lds_handoff();
-#pragma unroll
-        for (int j = 0; j < Q; ++j) {
-            const int e = j * kWave + lane;
-            if (e >= a.E) continue;
-            if (!taken[e / a.group_size])
-                c[j] = -INFINITY;
-            else if (!by_value && c[j] > -INFINITY)
-                c[j] = static_cast<double>(z[j]);
-        }
-    } else if (!by_value) {
-#pragma unroll
-        for (int j = 0; j < Q; ++j)
-            if (c[j] > -INFINITY) c[j] = static_cast<double>(z[j]);
     }
+    lds_handoff();
+}
+// The groups taken, a bit each.
+__device__ __forceinline__ uint64_t exact_groups(const RouterArgs& a, const double* value, int lane) {
+    double b1 = -INFINITY, b2 = -INFINITY;  // lane g: of group g
+#pragma unroll 1
+    for (int i = 0; lane < a.groups && i < a.group_size; ++i) {
+        const double v = value[lane * a.group_size + i];
+        b2 = fmax(b2, fmin(b1, v));
+        b1 = fmax(b1, v);
+    }
+    const double mine = a.top2 ? b1 + b2 : b1;
+    int rank = 0;
+#pragma unroll 1
+    for (int h = 0; h < a.groups; ++h) {
+        const double o = __shfl(mine, h);
+        rank += o > mine || (o == mine && h < lane);
+    }
+    return __ballot(lane < a.groups && rank < a.topk_groups);
+}
+// The winners, of the groups `taken`.
+template <typename T, int Q>
+__device__ __forceinline__ void exact_row(const RouterArgs& a, int64_t t, double* value, uint64_t taken, int* winner,
+                                          int lane) {
+    exact_values<T, Q>(a, t, value, a.bias != nullptr, lane);
     for (int k = 0; k < a.K; ++k) {
         double best = -INFINITY;
-        int slot = 0;
-#pragma unroll
-        for (int j = 0; j < Q; ++j) {
-            if (c[j] > best) {
-                best = c[j];
-                slot = j;
+        int at = 0;
+#pragma unroll 1
+        for (int e = lane; e < a.E; e += kWave) {
+            const double v = value[e];
+            if (v > best && (a.groups <= 1 || ((taken >> (e / a.group_size)) & 1) != 0)) {
+                best = v;
+                at = e;
             }
         }
         const uint64_t key = best > -INFINITY ? order_key64(best) : 0;
@@ -226,20 +223,44 @@ __device__ __forceinline__ void exact_row(const RouterArgs& a, int64_t t, double
         const uint32_t top_lo = topk::wave_max_u32(hi == top_hi ? lo : 0);
         const bool mine = best > -INFINITY && hi == top_hi && lo == top_lo;
         // the lowest expert of equal ones
-        const uint32_t inv = topk::wave_max_u32(mine ? ~static_cast<uint32_t>(slot * kWave + lane) : 0);
+        const uint32_t inv = topk::wave_max_u32(mine ? ~static_cast<uint32_t>(at) : 0);
         const int e = inv == 0 ? -1 : static_cast<int>(~inv);
         if (lane == 0) winner[k] = e;
-#pragma unroll
-        for (int j = 0; j < Q; ++j)
-            if (j * kWave + lane == e) c[j] = -INFINITY;
+        if (mine && at == e) value[e] = -INFINITY;
+        lds_handoff();
     }
-    lds_handoff();
 }
 
-template <typename T, int L, int P>
+// P consecutive values from element i on; those past the row's E are -inf.  VEC:
+// in pieces of up to 16 bytes, which E is a multiple of.
+template <typename T, int P, bool VEC>
+__device__ __forceinline__ void load_values(const void* p, int64_t i, int left, float (&f)[P]) {
+    constexpr int N = VEC ? (P < 16 / T::kBytes ? P : 16 / T::kBytes) : 1;
+#pragma unroll
+    for (int j = 0; j < P; j += N) {
+        float v[N];
+#pragma unroll
+        for (int k = 0; k < N; ++k) v[k] = -INFINITY;
+        if constexpr (N == 2) {
+            if (j < left) {
+                T::template load<1>(p, i + j, *reinterpret_cast<float(*)[1]>(&v[0]));
+                T::template load<1>(p, i + j + 1, *reinterpret_cast<float(*)[1]>(&v[1]));
+            }
+        } else {
+            if (j < left) T::template load<N>(p, i + j, v);
+        }
+#pragma unroll
+        for (int k = 0; k < N; ++k) f[j + k] = v[k];
+    }
+}
+
+// DEPTH: a lane's keys that can come up, the K largest and the next.
+template <typename T, int L, int P, int DEPTH, bool VEC>
 __global__ __launch_bounds__(kWaves* kWave) void router_kernel(RouterArgs a) {
-    constexpr int kRows = kWave / L;
-    constexpr int Q = L * P > kNarrowExperts ? L * P / kWave : kNarrowExperts / kWave;
+    constexpr int kRows = kWave / L, Q = (L * P + kWave - 1) / kWave;
+    constexpr uint32_t kCut = L == 16 ? 15 : 63;  // the key's bits that hold a slot or a lane
+    constexpr float kCutError = L == 16 ? 0x1p-19f : 0x1p-17f;  // of a value
+    static_assert(P <= 16 && L * P <= kMaxExperts, "slots");
     __shared__ WaveLds<L, P> lds[kWaves];
     const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
     const int sub = lane % L, row = lane / L;
@@ -250,221 +271,288 @@ __global__ __launch_bounds__(kWaves* kWave) void router_kernel(RouterArgs a) {
     const bool inside = t < a.num_tokens;
     const bool live = inside && (a.token_mask == nullptr || a.token_mask[t] != 0);
     const int64_t base = (inside ? t : first) * a.row_stride;
+    const bool by_value = a.bias != nullptr;
+    auto row_lanes = [](int r) { return L == kWave ? ~0ull : ((1ull << (L % kWave)) - 1) << (r * L); };
 
     float z[P], c[P];
+    load_values<T, P, VEC>(a.logits, base + sub * P, live ? a.E - sub * P : 0, z);
+    if (by_value) load_values<F32, P, VEC>(a.bias, sub * P, a.E - sub * P, c);
 #pragma unroll
-    for (int j = 0; j < P; ++j) {
-        const int e = j * L + sub;
-        float f[1] = {-INFINITY};
-        if (e < a.E) T::template load<1>(a.logits, base + e, f);
-        z[j] = live ? clean(f[0]) : -INFINITY;
-    }
+    for (int j = 0; j < P; ++j) z[j] = clean(z[j]);
     // the softmax's maximum and sum, where the order or the weights need them
-    const bool scored = a.bias != nullptr || (a.top2 && a.groups > 1);
-    float top = 0.0f, inv_sum = 0.0f, sum = 0.0f;
+    const bool scored = by_value || a.top2;
+    float top = 0.0f, inv_sum = 1.0f, sum = 1.0f;
     if (!a.sigmoid && (scored || !a.renormalize)) {
         top = z[0];
 #pragma unroll
         for (int j = 1; j < P; ++j) top = fmaxf(top, z[j]);
         top = group_max_f32<L>(top);
-        const float at = top > -INFINITY ? top : 0.0f;  // a row of nothing: every exponential is 0
+        if (top == -INFINITY) top = 0.0f;  // a row of nothing: every exponential is 0
+        sum = 0.0f;
 #pragma unroll
-        for (int j = 0; j < P; ++j) {
-            c[j] = exp_nonpos(z[j] - at);
-            sum += c[j];
-        }
+        for (int j = 0; j < P; ++j) sum += exp_nonpos(z[j] - top);
         sum = group_sum_f32<L>(sum);
-        inv_sum = 1.0f / sum;
-        top = at;
+        inv_sum = __builtin_amdgcn_rcpf(sum);
     }
     if (scored) {
 #pragma unroll
         for (int j = 0; j < P; ++j) {
-            const int e = j * L + sub;
-            const float s = a.sigmoid ? sigmoid_key(z[j]) : c[j] * inv_sum;
-            float b = 0.0f;
-            if (a.bias != nullptr && e < a.E) b = a.bias[e];
-            c[j] = (z[j] > -INFINITY && b > -INFINITY) ? s + fminf(b, FLT_MAX) : -INFINITY;
+            float s = a.sigmoid ? sigmoid_key(z[j]) : exp_nonpos(z[j] - top) * inv_sum;
+            if (by_value) s = c[j] > -INFINITY ? s + fminf(c[j], FLT_MAX) : -INFINITY;
+            c[j] = z[j] > -INFINITY ? s : -INFINITY;
         }
     } else {
 #pragma unroll
         for (int j = 0; j < P; ++j) c[j] = z[j];
     }
-    // two values closer than this may be in the other order: each key is cut
-    // by up to 2^-19 of its value, and errs by the rounding of c, 4 ulp of s
-    // (a softmax's sum of 16 terms a lane: 2^-19 of the largest s, which is
-    // 1 / sum) and the sigmoid's exponent, whose error times s is below 2^-22
-    const float most = a.sigmoid ? 1.0f : inv_sum;
-    const float slack = scored ? 0x1p-17f * most + (a.sigmoid ? 0x1p-22f : 0.0f) : 0.0f;
-    bool near = false;
+    // Two values closer than this may be in the other order: twice the sigmoid's
+    // error, or that of a softmax's score (its sum of up to 16 terms a lane and the
+    // steps over the lanes: below 2^-19 of the largest, which is 1 / sum), and the
+    // rounding of c, which the callers add with the cut of the keys.
+    const float slack = scored ? (a.sigmoid ? 0x1p-21f : 0x1p-17f * inv_sum) : 0.0f;
+    bool open = true;        // this lane's experts can be taken (of whole-lane groups)
+    uint64_t taken = ~0ull;  // the row's groups, a bit each
 
     if (a.groups > 1) {
-        float* value = reinterpret_cast<float*>(m.value) + row * a.E;
-#pragma unroll
-        for (int j = 0; j < P; ++j)
-            if (j * L + sub < a.E) value[j * L + sub] = c[j];
-        lds_handoff();
-        // several lanes scan a group where there are more lanes than groups
-        const int lpg = a.lanes_per_group, per_pass = L / lpg, part = sub % lpg;
-        float kept = INFINITY, left = -INFINITY;
-        float mine[L == 16 ? 4 : 1];
-#pragma unroll
-        for (int pass = 0; pass < (L == 16 ? 4 : 1); ++pass) {
-            const int g = pass * per_pass + sub / lpg;
+        float kept = INFINITY, left = -INFINITY;  // the worst group taken, the best left
+        const int n = a.lanes_per_group;
+        if (a.whole_lanes) {
             float b1 = -INFINITY, b2 = -INFINITY;
-            if (pass * per_pass < a.groups) {
+#pragma unroll
+            for (int j = 0; j < P; ++j) {
+                b2 = fmaxf(b2, fminf(b1, c[j]));
+                b1 = fmaxf(b1, c[j]);
+            }
+            const int g = sub / n;
+            if (n > 1) {
+                float2* each = reinterpret_cast<float2*>(m.best[row]);
+                each[sub] = make_float2(b1, b2);
+                lds_handoff();
+                for (int i = 0; i < n; ++i) {
+                    const float2 o = each[min(g * n + i, L - 1)];  // lanes past the last group: any
+                    const float lo = i == 0 ? -INFINITY : fminf(b1, o.x);
+                    b2 = i == 0 ? o.y : fmaxf(fmaxf(b2, o.y), lo);
+                    b1 = i == 0 ? o.x : fmaxf(b1, o.x);
+                }
+                lds_handoff();
+            }
+            const float mine = a.top2 ? b1 + b2 : b1;
+            float* score = m.best[row];
+            if (g < a.groups) score[g] = mine;  // the same from every lane of a group
+            lds_handoff();
+            int rank = 0;
+            for (int h = 0; h < a.groups; ++h) {
+                const float o = score[h];
+                rank += o > mine || (o == mine && h < g);
+            }
+            open = g < a.groups && rank < a.topk_groups;
+            if (open) kept = mine;
+            else if (g < a.groups)
+                left = mine;
+        } else {
+            float* value = reinterpret_cast<float*>(m.value) + row * a.E;
+#pragma unroll
+            for (int j = 0; j < P; ++j)
+                if (sub * P + j < a.E) value[sub * P + j] = c[j];
+            lds_handoff();
+            // several lanes scan a group where there are more lanes than groups
+            const int part = sub % n;
+            for (int g = sub / n; g < kMaxGroups; g += L / n) {
+                float b1 = -INFINITY, b2 = -INFINITY;
                 if (g < a.groups) {
-                    // every lane starts elsewhere in its group: other banks
-                    int i = part + lpg * (lane % ((a.group_size + lpg - 1) / lpg));
-                    for (int n = part; n < a.group_size; n += lpg) {
-                        if (i >= a.group_size) i = part;
+                    for (int i = part; i < a.group_size; i += n) {
                         const float v = value[g * a.group_size + i];
                         b2 = fmaxf(b2, fminf(b1, v));
                         b1 = fmaxf(b1, v);
-                        i += lpg;
                     }
                 }
-                for (int o = 1; o < lpg; o *= 2) {
+                for (int o = 1; o < n; o *= 2) {
                     const float o1 = __shfl_xor(b1, o), o2 = __shfl_xor(b2, o);
                     b2 = fmaxf(fmaxf(b2, o2), fminf(b1, o1));
                     b1 = fmaxf(b1, o1);
                 }
+                if (g < a.groups && part == 0) m.best[row][g] = a.top2 ? b1 + b2 : b1;
+                if (n > 1) break;  // then the lanes cover the groups at once
             }
-            mine[pass] = a.top2 ? b1 + b2 : b1;
-        }
-        // ranks over the row's groups; the scores pass through `taken`
-        float* score = reinterpret_cast<float*>(m.taken[row]);
+            lds_handoff();
+            taken = 0;
 #pragma unroll
-        for (int pass = 0; pass < (L == 16 ? 4 : 1); ++pass) {
-            const int g = pass * per_pass + sub / lpg;
-            if (g < a.groups && part == 0) score[g] = mine[pass];
-        }
-        lds_handoff();
-        bool in[L == 16 ? 4 : 1];
-#pragma unroll
-        for (int pass = 0; pass < (L == 16 ? 4 : 1); ++pass) {
-            const int g = pass * per_pass + sub / lpg;
-            in[pass] = false;
-            if (g < a.groups) {
-                int rank = 0;
-                for (int h = 0; h < a.groups; ++h) {
-                    const float o = score[h];
-                    rank += o > mine[pass] || (o == mine[pass] && h < g);
+            for (int i = 0; i < kMaxGroups / L; ++i) {
+                const int g = i * L + sub;
+                bool in = false;
+                if (g < a.groups) {
+                    const float mine = m.best[row][g];
+                    int rank = 0;
+                    for (int h = 0; h < a.groups; ++h) {
+                        const float o = m.best[row][h];
+                        rank += o > mine || (o == mine && h < g);
+                    }
+                    in = rank < a.topk_groups;
+                    if (in) kept = fminf(kept, mine);
+                    else
+                        left = fmaxf(left, mine);
                 }
-                in[pass] = rank < a.topk_groups;
-                if (in[pass]) kept = fminf(kept, mine[pass]);
-                else
-                    left = fmaxf(left, mine[pass]);
+                taken |= ((__ballot(in) >> (row * L)) & (L == kWave ? ~0ull : (1ull << L) - 1)) << (i * L % kWave);
             }
         }
-        lds_handoff();
-#pragma unroll
-        for (int pass = 0; pass < (L == 16 ? 4 : 1); ++pass) {
-            const int g = pass * per_pass + sub / lpg;
-            if (g < a.groups && part == 0) m.taken[row][g] = in[pass];
+        if (scored) {  // logits are compared as they are
+            kept = -group_max_f32<L>(-kept);
+            left = group_max_f32<L>(left);
+            // two sums of two values each, not cut to a key
+            uint64_t todo =
+                __ballot(left > -INFINITY && !(kept - left > 0x1p-21f * (fabsf(kept) + fabsf(left)) + 2 * slack));
+            while (todo != 0) {
+                const int r = __builtin_ctzll(todo) / L;
+                exact_values<T, Q>(a, first + r, m.value, true, lane);
+                const uint64_t of_row = exact_groups(a, m.value, lane);
+                lds_handoff();
+                if (row == r) {
+                    taken = of_row;
+                    open = !a.whole_lanes || ((of_row >> (sub / n)) & 1) != 0;
+                }
+                todo &= ~row_lanes(r);
+            }
         }
-        lds_handoff();
-        kept = -group_max_f32<L>(-kept);
-        left = group_max_f32<L>(left);
-        // two sums of two values each, not cut to a key
-        near = scored && left > -INFINITY && !(kept - left > 0x1p-21f * (fabsf(kept) + fabsf(left)) + 2 * slack);
+        if (!a.whole_lanes) {
 #pragma unroll
-        for (int j = 0; j < P; ++j) {
-            const int e = j * L + sub;
-            if (e < a.E) {
+            for (int j = 0; j < P; ++j) {
+                const int e = sub * P + j;
                 const int g = a.group_size > 1 ? __umulhi(static_cast<uint32_t>(e), a.group_magic) : e;
-                if (!m.taken[row][g]) c[j] = -INFINITY;
+                if (e < a.E && ((taken >> g) & 1) == 0) c[j] = z[j] = -INFINITY;
             }
         }
     }
-    // without a bias the logits order as the scores do, and exactly
-    const bool by_value = a.bias != nullptr;
+    if (!by_value) {  // the logits order as the scores do, and exactly
+#pragma unroll
+        for (int j = 0; j < P; ++j) c[j] = z[j];
+    }
     uint32_t key[P];
 #pragma unroll
-    for (int j = 0; j < P; ++j) {
-        const float v = by_value ? c[j] : z[j];
-        key[j] = c[j] > -INFINITY ? (order_key(v) & ~kSlotMask) | (kSlotMask - j) : kNone;
-    }
+    for (int j = 0; j < P; ++j) key[j] = (order_key(c[j]) & ~kCut) | (kCut - j);
     sort_desc<P>(key);
 
-    uint32_t my_key = kNone;
+    uint32_t my_key = 0, best = 0;
     m.winner[row][sub % 16] = -1;
     lds_handoff();
     for (int k = 0; k < a.K; ++k) {
-        const uint32_t best = group_max_u32<L>(key[0]);
-        const bool hit = key[0] == best && best != kNone;
-        const uint64_t who = __ballot(hit);
-        // the lowest lane of the row's that hold it
-        const uint64_t below = who & ((L == kWave ? ~0ull : ((1ull << L) - 1) << (row * L)) & ((1ull << lane) - 1));
+        const uint32_t head = open ? (key[0] & ~kCut) | (kCut - sub) : 0;
+        best = group_max_u32<L>(head);
         if (sub == k) my_key = best;
-        if (hit && below == 0) {
-            m.winner[row][k] = static_cast<int>(kSlotMask - (key[0] & kSlotMask)) * L + sub;
+        if (head == best && best > kNone) {
+            m.winner[row][k] = sub * P + static_cast<int>(kCut - (key[0] & kCut));
 #pragma unroll
-            for (int j = 0; j + 1 < P; ++j) key[j] = key[j + 1];
-            key[P - 1] = kNone;
+            for (int j = 0; j < DEPTH && j + 1 < P; ++j) key[j] = key[j + 1];
+            if (DEPTH >= P) key[P - 1] = 0;
         }
     }
     lds_handoff();
 
-    // is the order proven?
-    {
-        const int e = sub < 16 ? m.winner[row][sub] : -1;
-        float ze = -INFINITY, be = 0.0f;
-        if (sub < a.K && e >= 0) {
-            float f[1];
-            T::template load<1>(a.logits, base + e, f);
-            ze = clean(f[0]);
-            if (by_value) be = a.bias[e];
-        }
-        const uint32_t cut = my_key & ~kSlotMask;
-        const float v = key_value(cut);
-        // the next winner, one lane up
-        const uint32_t next = __shfl_down(my_key, 1) & ~kSlotMask;
-        const float zn = __shfl_down(ze, 1), bn = __shfl_down(be, 1);
-        const bool exact_keys = !by_value && T::kBytes == 2;  // bf16 logits lose nothing
-        if (!exact_keys && sub + 1 < a.K && next != kNone) {
-            const bool same = ze == zn && be == bn;
-            const float vn = key_value(next);
-            const bool close =
-                by_value ? v - vn <= 0x1p-18f * (fabsf(v) + fabsf(vn)) + slack : cut == next;
-            near = near || (close && !same);
-        }
-        // what is left within the last winner's reach has to be equal to it
-        const int last = row * L + a.K - 1;
-        const uint32_t cut_last = __shfl(cut, last);
-        const float z_last = __shfl(ze, last), b_last = __shfl(be, last);
-        if (!exact_keys && cut_last != kNone) {
-            const float vl = key_value(cut_last);
-            const uint32_t reach =
-                by_value ? order_key(vl - (0x1p-16f * fabsf(vl) + 2 * slack)) & ~kSlotMask : cut_last;
-            for (int j = 0; j < P; ++j) {
-                if (key[0] < reach || key[0] == kNone) break;
-                const int o = static_cast<int>(kSlotMask - (key[0] & kSlotMask)) * L + sub;
-                float f[1];
-                T::template load<1>(a.logits, base + o, f);
-                near = near || clean(f[0]) != z_last || (by_value && a.bias[o] != b_last);
+    // Is the order proven?  Not where the next winner, one lane up, or something
+    // left is within the reach of this one; then they have to be equal bit by bit.
+    bool near = false;
+    if (by_value || T::kBytes == 4) {  // keys of bf16 logits lose nothing
+        const uint32_t cut = my_key & ~kCut, next = dpp_u32<kDppRowShl1>(my_key) & ~kCut;
+        const float v = key_value(cut), vn = key_value(next);
+        const bool pair =
+            sub + 1 < a.K && next > kNone &&
+            (by_value ? !(v - vn > (kCutError + 0x1p-23f) * (fabsf(v) + fabsf(vn)) + slack) : cut == next);
+        const uint32_t last = best & ~kCut;
+        const float vl = key_value(last);
+        const uint32_t reach =
+            by_value ? order_key(vl - ((2 * kCutError + 0x1p-22f) * 2 * fabsf(vl) + 2 * slack)) & ~kCut : last;
+        const bool rest = open && best > kNone && key[0] > kNone && (key[0] & ~kCut) >= reach;
+        if (__ballot(pair || rest) != 0) {
+            int e = sub < 16 ? m.winner[row][sub] : -1;
+            float ze = -INFINITY, be = 0.0f;
+            if (sub < a.K && e >= 0) {
+                ze = logit<T>(a, base + e);
+                if (by_value) be = a.bias[e];
+            }
+            const float zn = dpp_f32<kDppRowShl1>(ze), bn = dpp_f32<kDppRowShl1>(be);
+            bool again = pair && !(ze == zn && be == bn);
+            const int from = row * L + a.K - 1;
+            const float z_last = __shfl(ze, from), b_last = __shfl(be, from);
+            int found = 0, candidate = -1;  // left, within reach, and not equal to the last
+            for (int j = 0; rest && j < P; ++j) {
+                if (key[0] <= kNone || (key[0] & ~kCut) < reach) break;
+                if (j == DEPTH) {
+                    found = 2;  // more than the lane has kept: as good as several
+                    break;
+                }
+                const int o = sub * P + static_cast<int>(kCut - (key[0] & kCut));
+                if (logit<T>(a, base + o) != z_last || (by_value && a.bias[o] != b_last)) {
+                    ++found;
+                    candidate = o;
+                }
 #pragma unroll
                 for (int i = 0; i + 1 < P; ++i) key[i] = key[i + 1];
-                key[P - 1] = kNone;
+                key[P - 1] = 0;
+            }
+            const uint64_t mine_only = row_lanes(row);
+            const uint64_t with = __ballot(found > 0) & mine_only;
+            const bool many = (__ballot(found > 1) & mine_only) != 0 || (with & (with - 1)) != 0;
+            again = (__ballot(again || found > 0) & mine_only) != 0;  // of the row
+            near = near || (many && again) || (with != 0 && a.K == 16);
+            if (__ballot(again && !near) != 0) {
+                // the candidate is one more, in lane K
+                if (found == 1 && !near) m.winner[row][a.K] = candidate;
+                lds_handoff();
+                const bool in = again && !near && sub <= a.K && sub < 16;
+                e = in ? m.winner[row][sub] : -1;
+                if (in && sub == a.K && e >= 0) {
+                    ze = logit<T>(a, base + e);
+                    if (by_value) be = a.bias[e];
+                }
+                double high = 0.0, total = 1.0;
+                if (by_value && !a.sigmoid) {
+                    high = static_cast<double>(top);
+                    total = 0.0;
+#pragma unroll 1
+                    for (int o = sub; o < a.E; o += L) {
+                        const float f = live ? logit<T>(a, base + o) : -INFINITY;
+                        if (f > -INFINITY) total += exp(static_cast<double>(f) - high);
+                    }
+                    for (int o = 1; o < L; o *= 2) total += __shfl_xor(total, o);
+                }
+                double value = static_cast<double>(ze);
+                if (by_value) {
+                    const double x = exp(a.sigmoid ? -value : value - high);
+                    value = (a.sigmoid ? 1.0 / (1.0 + x) : x / total) + static_cast<double>(fminf(be, FLT_MAX));
+                }
+                if (e < 0) value = -INFINITY;
+                int rank = 0;
+                for (int k = 0; k <= a.K && k < 16; ++k) {
+                    const double o = __shfl(value, row * L + k);
+                    const int oe = __shfl(e, row * L + k);
+                    rank += oe >= 0 && (o > value || (o == value && oe < e));
+                }
+                if (e >= 0 && rank < 16) m.winner[row][rank] = e;
+                lds_handoff();
             }
         }
-        uint64_t todo = __ballot(near);
-        while (todo != 0) {
-            const int r = __builtin_ctzll(todo) / L;
-            exact_row<T, Q>(a, first + r, m.value, m.group, m.taken[r], m.winner[r], lane);
-            todo &= L == kWave ? 0 : ~(((1ull << L) - 1) << (r * L));
+    }
+    uint64_t todo = __ballot(near);
+    while (todo != 0) {
+        const int r = __builtin_ctzll(todo) / L;
+        uint64_t groups = taken;  // of row r
+        if (a.groups > 1) {
+            if (a.whole_lanes) {
+                groups = 0;
+                const uint64_t lanes = __ballot(open);
+                for (int g = 0; g < a.groups; ++g) groups |= ((lanes >> (r * L + g * a.lanes_per_group)) & 1) << g;
+            } else {
+                groups = __shfl(static_cast<unsigned long long>(taken), r * L);
+            }
         }
+        exact_row<T, Q>(a, first + r, m.value, groups, m.winner[r], lane);
+        todo &= ~row_lanes(r);
     }
 
     // the weights, lane k of a row its k-th
     const int e = sub < 16 ? m.winner[row][sub] : -1;
     const bool mine = sub < a.K && e >= 0;
     float ze = -INFINITY;
-    if (mine) {
-        float f[1];
-        T::template load<1>(a.logits, base + e, f);
-        ze = clean(f[0]);
-    }
+    if (mine) ze = logit<T>(a, base + e);
     float w = 0.0f;
     if (a.renormalize) {
         // shifted by the largest logit chosen, so that a row whose scores all
@@ -624,27 +712,44 @@ __global__ __launch_bounds__(kWaves* kWave) void router_backward_kernel(Backward
     }
 }
 
-template <typename T, int L, int P>
-void launch_router_shape(const RouterArgs& a, hipStream_t stream) {
+template <typename T, int L, int P, int DEPTH, bool VEC>
+void launch_router_form(const RouterArgs& a, hipStream_t stream) {
     const int64_t per = kWaves * (kWave / L);
-    hipLaunchKernelGGL((router_kernel<T, L, P>), dim3(static_cast<unsigned>((a.num_tokens + per - 1) / per)),
-                       dim3(kWaves * kWave), 0, stream, a);
+    hipLaunchKernelGGL((router_kernel<T, L, P, DEPTH, VEC>),
+                       dim3(static_cast<unsigned>((a.num_tokens + per - 1) / per)), dim3(kWaves * kWave), 0, stream, a);
+}
+
+template <typename T, int L, int P>
+hipError_t launch_router_shape(RouterArgs a, hipStream_t stream) {
+    // a group of whole lanes; or the lanes, a power of two, that share the scan of one
+    a.whole_lanes = a.group_size % P == 0;
+    a.lanes_per_group = a.whole_lanes ? a.group_size / P : 1;
+    while (!a.whole_lanes && a.lanes_per_group * 2 * a.groups <= L && a.lanes_per_group * 2 <= a.group_size)
+        a.lanes_per_group *= 2;
+    constexpr int N = P < 16 / T::kBytes ? P : 16 / T::kBytes, B = P < 4 ? P : 4;
+    const bool vec = a.E % (N > B ? N : B) == 0 && a.row_stride % N == 0 && aligned(a.logits, N * T::kBytes) &&
+                     aligned(a.bias, 4 * B);
+    constexpr int kFew = P > 8 ? 8 : P;  // the usual K: half the moves when a lane's key has been taken
+    if (a.K <= kFew) {
+        if (vec) launch_router_form<T, L, P, kFew, true>(a, stream);
+        else
+            launch_router_form<T, L, P, kFew, false>(a, stream);
+    } else if (vec) {
+        launch_router_form<T, L, P, P, true>(a, stream);
+    } else {
+        launch_router_form<T, L, P, P, false>(a, stream);
+    }
+    return hipGetLastError();
 }
 
 template <typename T>
 hipError_t launch_router(const RouterArgs& a, hipStream_t stream) {
-    if (a.E <= 32) launch_router_shape<T, 16, 2>(a, stream);
-    else if (a.E <= 64)
-        launch_router_shape<T, 16, 4>(a, stream);
-    else if (a.E <= 128)
-        launch_router_shape<T, 16, 8>(a, stream);
-    else if (a.E <= kNarrowExperts)
-        launch_router_shape<T, 16, 16>(a, stream);
-    else if (a.E <= 512)
-        launch_router_shape<T, 64, 8>(a, stream);
-    else
-        launch_router_shape<T, 64, 16>(a, stream);
-    return hipGetLastError();
+    if (a.E <= 32) return launch_router_shape<T, 16, 2>(a, stream);
+    if (a.E <= 64) return launch_router_shape<T, 16, 4>(a, stream);
+    if (a.E <= 128) return launch_router_shape<T, 16, 8>(a, stream);
+    if (a.E <= kNarrowExperts) return launch_router_shape<T, 16, 16>(a, stream);
+    if (a.E <= 512) return launch_router_shape<T, 64, 8>(a, stream);
+    return launch_router_shape<T, 64, 16>(a, stream);
 }
 
 template <typename T, int L, bool VEC>
@@ -703,9 +808,6 @@ extern "C" moe_status moe_router(const void* logits, int32_t logits_dtype, int64
     if (!aligned(logits, logits_dtype == MOE_DTYPE_BF16 ? 2 : 4) || !aligned(bias, 4) || !aligned(topk_idx, 8) ||
         !aligned(topk_weights, 4))
         return MOE_ERR_INVALID_ARGUMENT;
-    const int L = num_experts <= kNarrowExperts ? 16 : kWave;
-    int lanes = 1;
-    while (lanes * 2 * num_groups <= L && lanes * 2 <= size) lanes *= 2;
     RouterArgs a{};
     a.logits = logits;
     a.row_stride = row_stride;
@@ -718,7 +820,6 @@ extern "C" moe_status moe_router(const void* logits, int32_t logits_dtype, int64
     a.topk_groups = topk_groups;
     a.group_size = size;
     a.top2 = a.groups > 1 && group_score == MOE_GROUP_TOP2;
-    a.lanes_per_group = lanes;
     // exact for e < 2^16: the excess of the rounded-up reciprocal is below 2^-32, times e below 1 / size
     a.group_magic = size > 1 ? static_cast<uint32_t>(0xFFFFFFFFu / static_cast<uint32_t>(size) + 1) : 0;
     a.renormalize = renormalize;
