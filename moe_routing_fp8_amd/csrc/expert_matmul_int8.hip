@@ -497,12 +497,33 @@ __global__ __launch_bounds__(WM* WN* kWave) void expert_matmul_int8_kernel(Matmu
     }
 }
 
-// Sixteen bytes at any address; past `left` bytes zeros.
+// A row's sixteen bytes from p on, at any address, of which `left` (or fewer, or
+// none) are the row's: those before its end instead where it ends sooner, so that
+// no byte outside it is read and no lane takes another path.
 struct __attribute__((packed, aligned(1))) Unaligned16 {
     u32x4_t v;
 };
-__device__ __forceinline__ u32x4_t load_any(const uint8_t* p, int left) {
-    if (left >= 16) return reinterpret_cast<const Unaligned16*>(p)->v;
+__device__ __forceinline__ u32x4_t load_odd(const uint8_t* p, int left) {
+    return reinterpret_cast<const Unaligned16*>(p + min(left - 16, 0))->v;
+}
+// Those bytes in their places, with zeros behind the row's end.
+__device__ __forceinline__ u32x4_t shift_odd(u32x4_t v, int left) {
+    const int n = 16 - min(max(left, 0), 16);  // bytes that came before p
+    u32x4_t r;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        uint32_t lo = 0, hi = 0;  // words i + n / 4 and the next
+#pragma unroll
+        for (int k = i; k < 4; ++k) {
+            lo = k == i + n / 4 ? v[k] : lo;
+            hi = k == i + n / 4 + 1 ? v[k] : hi;
+        }
+        r[i] = __builtin_amdgcn_alignbyte(hi, lo, n % 4);
+    }
+    return r;
+}
+// The same of a row of fewer than sixteen bytes, byte by byte.
+__device__ __forceinline__ u32x4_t load_short(const uint8_t* p, int left) {
     u32x4_t v = {0, 0, 0, 0};
 #pragma unroll
     for (int i = 0; i < 15; ++i)
@@ -545,7 +566,7 @@ __global__ __launch_bounds__(WM* WN* kWave) void expert_matmul_int8_odd_kernel(M
         auto fetch = [&]() {
 #pragma unroll
             for (int j = 0; j < kLoads; ++j) {
-                held[j] = load_any(src[j], left[j]);
+                held[j] = a.K < 16 ? load_short(src[j], left[j]) : load_odd(src[j], left[j]);
                 src[j] += BK;
                 left[j] -= BK;
             }
@@ -561,8 +582,11 @@ __global__ __launch_bounds__(WM* WN* kWave) void expert_matmul_int8_odd_kernel(M
         for (int i = 0; i < steps; ++i) {
             uint8_t* s = stages[i & 1];
 #pragma unroll
-            for (int j = 0; j < kLoads; ++j)
-                *reinterpret_cast<u32x4_t*>(s + (wave + j * Y::kWaves) * 1024 + lane * 16) = held[j];
+            for (int j = 0; j < kLoads; ++j) {
+                u32x4_t v = held[j];
+                if (i + 1 == steps && a.K >= 16) v = shift_odd(v, left[j] + BK);
+                *reinterpret_cast<u32x4_t*>(s + (wave + j * Y::kWaves) * 1024 + lane * 16) = v;
+            }
             if (i + 1 < steps) fetch();
             __syncthreads();
             Y::multiply(s, s + BM * BK, used, wm, wn, lane, acc);
@@ -611,11 +635,15 @@ hipError_t launch_odd(MatmulArgs a, hipStream_t stream) {
 hipError_t launch_matmul(const MatmulArgs& a, bool direct, hipStream_t stream) {
     const int64_t busy = a.E < a.num_rows ? a.E : a.num_rows, mean = (a.num_rows + busy - 1) / busy;
     auto tiles = [&](int64_t bm, int64_t bn) { return busy * ((mean + bm - 1) / bm) * ((a.N + bn - 1) / bn); };
+    const int64_t cus = device_cu_count();
     if (!direct) {
-        if (mean <= 16) return launch_odd<16, 64, 256, 1, 4>(a, stream);
+        // 700 rows of one matrix, 1000 -> 500: 8.8 against 10.4 us in tiles of 64 x 64; 5 experts of 156 rows, 1999 ->
+        // 1021, 800 of these: 26.8 against 17.4 us
+        if (mean <= 8 || tiles(16, 64) <= 2 * cus) return launch_odd<16, 64, 256, 1, 4>(a, stream);
+        // 16 experts of 125 rows, 3001 -> 1000: 34.5 against 43.3 us; those 5 experts, 80 of these: 25.6 us
+        if (tiles(128, 128) >= cus / 2) return launch_odd<128, 128, 128, 2, 4>(a, stream);
         return launch_odd<64, 64, 128, 2, 2>(a, stream);
     }
-    const int64_t cus = device_cu_count();
     // one tile holds most experts' rows (32 experts, 7168 -> 4096, 128 rows: 98 us; 108 us in tiles of 32 x 128), or
     // the places of two workgroups a compute unit are not all taken (256 rows of one matrix, 4096 -> 2048: 15.4
     // against 21.2 us; 1024 rows, 1024 -> 1024, two for each place: 11.5 against 8.9 us)
