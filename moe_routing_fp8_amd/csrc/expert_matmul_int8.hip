@@ -624,8 +624,10 @@ hipError_t launch_tiles(MatmulArgs a, hipStream_t stream) {
 template <int BM, int BN, int BK, int WM, int WN>
 hipError_t launch_odd(MatmulArgs a, hipStream_t stream) {
     a.n_tiles = (a.N + BN - 1) / BN;
-    hipLaunchKernelGGL((expert_matmul_int8_odd_kernel<BM, BN, BK, WM, WN>), dim3(whole_dies(most_tiles(a, BM))),
-                       dim3(WM * WN * kWave), 0, stream, a);
+    constexpr int64_t kPerCu = 8;  // more than fit at once
+    const int64_t places = device_cu_count() * kPerCu, tiles = most_tiles(a, BM);
+    hipLaunchKernelGGL((expert_matmul_int8_odd_kernel<BM, BN, BK, WM, WN>),
+                       dim3(whole_dies(tiles < places ? tiles : places)), dim3(WM * WN * kWave), 0, stream, a);
     return hipGetLastError();
 }
 

@@ -432,6 +432,7 @@ __global__ __launch_bounds__(kWaves* kWave) void router_kernel(RouterArgs a) {
     sort_desc<P>(key);
 
     uint32_t my_key = 0, best = 0;
+    lds_handoff();  // the groups' scores, in the same place, have been read
     m.winner[row][sub % 16] = -1;
     lds_handoff();
     for (int k = 0; k < a.K; ++k) {
