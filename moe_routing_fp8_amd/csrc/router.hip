@@ -295,12 +295,20 @@ __global__ __launch_bounds__(kWaves* kWave) void router_kernel(RouterArgs a) {
         inv_sum = __builtin_amdgcn_rcpf(sum);
     }
     if (scored) {
+        float s[P];
+        if (a.sigmoid) {
 #pragma unroll
-        for (int j = 0; j < P; ++j) {
-            float s = a.sigmoid ? sigmoid_key(z[j]) : exp_nonpos(z[j] - top) * inv_sum;
-            if (by_value) s = c[j] > -INFINITY ? s + fminf(c[j], FLT_MAX) : -INFINITY;
-            c[j] = z[j] > -INFINITY ? s : -INFINITY;
+            for (int j = 0; j < P; ++j) s[j] = sigmoid_key(z[j]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < P; ++j) s[j] = exp_nonpos(z[j] - top) * inv_sum;
         }
+        if (by_value) {
+#pragma unroll
+            for (int j = 0; j < P; ++j) s[j] = c[j] > -INFINITY ? s[j] + fminf(c[j], FLT_MAX) : -INFINITY;
+        }
+#pragma unroll
+        for (int j = 0; j < P; ++j) c[j] = z[j] > -INFINITY ? s[j] : -INFINITY;
     } else {
 #pragma unroll
         for (int j = 0; j < P; ++j) c[j] = z[j];
