@@ -303,17 +303,20 @@ __device__ __forceinline__ void wait_loads() {
 // read of LDS (a large matrix: 1230 against 1010 us); here wait_loads and the
 // barrier behind it order them.  No register is written, so there is no output
 // that the compiler could take as ready; m0's write needs one wait state.
-__device__ __forceinline__ uint32_t lds_address(const void* lds) {
-    return static_cast<uint32_t>(reinterpret_cast<uintptr_t>((const __attribute__((address_space(3))) void*)lds));
-}
+// The LDS address, one for the wave, is that of a __shared__ array plus an offset.
+#define MOE_LDS_ADDRESS(array) \
+    static_cast<uint32_t>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) void*)(array)))
+
 #pragma clang diagnostic push
 #pragma clang diagnostic ignored "-Winline-asm"  // that m0 is named as overwritten
-__device__ __forceinline__ void load16_to_lds(const void* p, const void* lds) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds_address(lds)), "v"(p)
+__device__ __forceinline__ void load16_to_lds(const void* p, uint32_t lds) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(
+                     __builtin_amdgcn_readfirstlane(lds)), "v"(p)
                  : "memory", "m0");
 }
-__device__ __forceinline__ void load4_to_lds(const void* p, const void* lds) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(lds_address(lds)), "v"(p)
+__device__ __forceinline__ void load4_to_lds(const void* p, uint32_t lds) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(
+                     __builtin_amdgcn_readfirstlane(lds)), "v"(p)
                  : "memory", "m0");
 }
 #pragma clang diagnostic pop
@@ -341,6 +344,8 @@ __global__ __launch_bounds__(WM* WN* kWave) void expert_matmul_int8_kernel(Matmu
     __shared__ float x_scale[SW][kScales], w_scale[SW][BN];
     __shared__ uint8_t known[SW][BM];
     __shared__ Tile tiles_ahead[SW];
+    const uint32_t x_lds = MOE_LDS_ADDRESS(x_stages), w_lds = MOE_LDS_ADDRESS(w_stages);
+    const uint32_t x_scale_lds = MOE_LDS_ADDRESS(x_scale), w_scale_lds = MOE_LDS_ADDRESS(w_scale);
 
     const Tiles<BM, BN> tiles(a);
     // workgroups go to the dies in turn; a die's take one run of tiles by turns
@@ -388,7 +393,7 @@ __global__ __launch_bounds__(WM* WN* kWave) void expert_matmul_int8_kernel(Matmu
             if (threadIdx.x == 0) tiles_ahead[x_slot] = after;
             if (wave * kWave < BM)
                 load4_to_lds(has ? static_cast<const void*>(a.x_sf + my_token) : &kZeroChunk,
-                             &x_scale[x_slot][wave * kWave]);
+                             x_scale_lds + (x_slot * kScales + wave * kWave) * 4);
         }
 #pragma unroll
         for (int j = 0; j < kX; ++j) {
@@ -399,7 +404,7 @@ __global__ __launch_bounds__(WM* WN* kWave) void expert_matmul_int8_kernel(Matmu
                 if (x_step * BK + (line_chunk ^ Y::x_swizzle(r)) * 16 >= a.K)
                     p = reinterpret_cast<const uint8_t*>(&kZeroChunk);
             }
-            load16_to_lds(p, x_stages[x_stage] + (wave + j * kWaves) * 1024);
+            load16_to_lds(p, x_lds + x_stage * (BM * BK) + (wave + j * kWaves) * 1024);
             x_src[j] += BK;
         }
         x_stage = x_stage + 1 == SX ? 0 : x_stage + 1;
@@ -420,7 +425,9 @@ __global__ __launch_bounds__(WM* WN* kWave) void expert_matmul_int8_kernel(Matmu
 #pragma unroll
             for (int i = 0; i < (BN + kThreads - 1) / kThreads; ++i) {
                 const int c = i * kThreads + wave * kWave;
-                if (c < BN) load4_to_lds(a.w_sf + first + min(next.channel + c + lane, a.N - 1), &w_scale[w_slot][c]);
+                if (c < BN)
+                    load4_to_lds(a.w_sf + first + min(next.channel + c + lane, a.N - 1),
+                                 w_scale_lds + (w_slot * BN + c) * 4);
             }
         }
 #pragma unroll
@@ -431,7 +438,7 @@ __global__ __launch_bounds__(WM* WN* kWave) void expert_matmul_int8_kernel(Matmu
                 if (w_step * BK + (line_chunk ^ Y::w_swizzle(r)) * 16 >= a.K)
                     p = reinterpret_cast<const uint8_t*>(&kZeroChunk);
             }
-            load16_to_lds(p, w_stages[w_stage] + (wave + j * kWaves) * 1024);
+            load16_to_lds(p, w_lds + w_stage * (BN * BK) + (wave + j * kWaves) * 1024);
             w_src[j] += BK;
         }
         if (SX != SW && w_step == 0) read_tokens(next);  // x comes to this tile one step later
