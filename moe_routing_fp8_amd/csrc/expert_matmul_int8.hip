@@ -659,8 +659,9 @@ hipError_t launch_matmul(const MatmulArgs& a, bool direct, hipStream_t stream) {
     if (mean <= 8 || tiles(16, 64) <= 2 * cus) return launch_tiles<16, 64, 256, 3, 3, 1, 4, 2>(a, stream);
     // 32 experts, 7168 -> 4096, 1024 rows an expert: 1060 against 1120 us in the next; 512: 635 against 596 us
     if (mean > 768 && tiles(256, 256) >= 2 * cus) return launch_tiles<256, 256, 128, 2, 2, 2, 4, 1>(a, stream);
-    // the same, 512 rows: 597 against 624 us in the next; 128 rows: 272 against 246 us
-    if (mean > 256 && tiles(192, 256) >= cus) return launch_tiles<192, 256, 128, 2, 3, 2, 4, 1>(a, stream);
+    // the same, 512 rows: 598 against 668 us in the next; 8192 rows over 32 experts, 2048 -> 7168: 212 against 224 us;
+    // 128 rows, 7168 -> 4096: 306 against 288 us
+    if (mean > 192 && tiles(192, 256) >= cus) return launch_tiles<192, 256, 128, 2, 3, 2, 4, 1>(a, stream);
     // the same, 64 rows: 191 against 218 us in the next; 2048 rows of one matrix, 2048 -> 2048, 128 tiles of this
     // size: 23.1 against 20.6 us
     if (tiles(128, 256) >= cus) return launch_tiles<128, 256, 128, 3, 3, 2, 4, 1>(a, stream);
