@@ -670,7 +670,8 @@ moe_status moe_expert_matvec(const void* x, int32_t x_dtype, const float* x_sf, 
  *
  * logits         logits_dtype [T, E], rows row_stride elements apart.
  * logits_dtype   MOE_DTYPE_BF16 or MOE_DTYPE_F32.
- * num_tokens     0 <= T <= (2^31 - 1) / 16.
+ * num_tokens     0 <= T <= (2^31 - 1) / 16; below 2^26 with more than 256
+ *                experts (else: MOE_ERR_UNSUPPORTED).
  * num_experts    E, 1 <= E <= 1024.
  * num_topk       K, 1 <= K <= min(16, topk_groups * E / num_groups).
  * bias           fp32 [E], or NULL.
@@ -680,8 +681,8 @@ moe_status moe_expert_matvec(const void* x, int32_t x_dtype, const float* x_sf, 
  * group_score    MOE_GROUP_MAX or MOE_GROUP_TOP2 (with more than one group it
  *                needs groups of at least two experts).
  * scale          finite.
- * token_mask     uint8 [T], 0 = masked (the token's logits may hold anything;
- *                their memory is still read), or NULL.
+ * token_mask     uint8 [T], 0 = masked (the token's logits may hold
+ *                anything), or NULL.
  * topk_idx       int64 [T, K] output;  topk_weights fp32 [T, K] output.
  */
 moe_status moe_router(const void* logits, int32_t logits_dtype, int64_t row_stride, int64_t num_tokens,

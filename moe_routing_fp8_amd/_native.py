@@ -1153,7 +1153,7 @@ def _int8_outputs(R, width, dev, out, stream):
 
 def moe_cast_int8(x: torch.Tensor, out=None, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
     """Rows bf16 or fp32 [R, H] (any row stride) -> (codes int8 [R, H], scales fp32 [R]): one scale a row, its
-    largest magnitude / 127."""
+    largest magnitude / 127.  (Debug mode checks contiguous bf16 rows.)"""
     stride = _need_rows(x, "x")
     R, H = x.shape
     dev = x.device

@@ -195,6 +195,74 @@ def test_uneven_experts():
     _check(_case([1] * 1000 + [30] + [0] * 23, 16, 64))
 
 
+def _device_check(s, dtype):
+    """As _check, the whole-number sums as 64-bit products on the device."""
+    c = {k: v.cuda() if v is not None else None for k, v in s.items()}
+    R, N = int(s["off"][-1]), s["w"].shape[1]
+    out = torch.full((R, N), 7.0, dtype=dtype, device="cuda")
+    y = moe.moe_expert_matmul_int8(c["x"], c["x_sf"], c["w"], c["w_sf"], expert_offsets=c["off"],
+                                   row_token=c["row_token"], out=out)
+    at = c["row_token"].long() if c["row_token"] is not None else torch.arange(R, device="cuda")
+    known = (at >= 0) & (at < c["x"].shape[0])
+    at = at.clamp(0, c["x"].shape[0] - 1)
+    ends = s["off"].tolist()
+    for e in range(len(ends) - 1):
+        rows = slice(ends[e], ends[e + 1])
+        sums = c["x"][at[rows]].double() @ c["w"][e].double().t().contiguous()
+        want = (sums.float() * c["x_sf"][at[rows], None]) * c["w_sf"][e]
+        assert torch.equal(y[rows], torch.where(known[rows, None], want, 0.0).to(dtype)), e
+
+
+# experts and channels for which each tile is chosen on 256 compute units: of 256 x 256, 192 x 256, 128 x 256, 64 x 128
+# and 32 x 128; k of one step, of steps and a part, and of many steps
+FORMS = [([9000, 0, 8500], 4104), ([0, 700, 200, 300, 1, 500, 250, 600], 5000), ([100, 40, 0, 190, 7] * 4, 3500),
+         ([300, 310, 20, 500], 1700), ([129, 0, 33], 600), ([700] * 2 + [0] * 70 + [300] * 2, 2304)]
+
+
+@pytest.mark.parametrize("counts,N", FORMS)
+@pytest.mark.parametrize("K", [16, 128, 272, 656])
+def test_product_in_every_tile(counts, N, K):
+    _log(f"{counts} N={N} K={K}")
+    _device_check(_case(counts, N, K), BF16)
+    s = _case(counts, N, K, by_token=True, seed=1)
+    s["row_token"][::97] = -1
+    _device_check(s, F32)
+
+
+@pytest.mark.parametrize("counts,N,K", [([700, 650], 1030, 33), ([125] * 16, 1000, 301), ([40, 0, 90], 200, 47)])
+def test_product_in_every_tile_at_odd_sizes(counts, N, K):
+    _device_check(_case(counts, N, K), BF16)
+    _device_check(_case(counts, N, K, by_token=True, seed=1), F32)
+
+
+def test_debug_mode_checks_activations(monkeypatch):
+    x = torch.ones(4, 64, dtype=BF16, device="cuda")
+    monkeypatch.setenv("MOE_FP8_DEBUG", "1")
+    moe.moe_cast_int8(x)
+    moe.swiglu_cast_int8(x)
+    x[2, 7] = float("nan")
+    for call in (moe.moe_cast_int8, moe.swiglu_cast_int8):
+        with pytest.raises(ValueError, match="MOE_CHECK_NONFINITE_ACTIVATION"):
+            call(x)
+
+
+def test_two_streams_at_once():
+    """Nothing is shared between calls: two sets of inputs in flight on two streams."""
+    sets = [_case([300, 20, 500], 1024, 1024, by_token=True, seed=i) for i in range(2)]
+    want = [_run(s) for s in sets]
+    held = [{k: v.cuda() for k, v in s.items()} for s in sets]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in sets]
+    got = [[], []]
+    for _ in range(5):
+        for i, (c, stream) in enumerate(zip(held, streams)):
+            got[i].append(moe.moe_expert_matmul_int8(c["x"], c["x_sf"], c["w"], c["w_sf"], expert_offsets=c["off"],
+                                                     row_token=c["row_token"], stream=stream))
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(y, want[i]) for y in got[i])
+
+
 def test_largest_codes_do_not_overflow():
     """-128 times -128 over the longest k: 131071 * 2^14 < 2^31."""
     K = 131071

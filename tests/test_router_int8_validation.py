@@ -40,6 +40,7 @@ def test_router(lib):
     assert call(G=16, kept=1, K=5) == INVALID                     # four experts cannot give five
     assert call(G=64, kept=64) == INVALID                         # the two best of one
     assert call(E=260, rs=260, G=65, kept=30) == UNSUPPORTED
+    assert call(T=1 << 26, E=264, rs=264) == UNSUPPORTED          # 2^32 threads
     assert call(z=None) == INVALID and call(idx=None) == INVALID and call(w=None) == INVALID
     assert call(z=FAKE + 2) == INVALID and call(dt=0, z=FAKE + 1) == INVALID
     assert call(bias=FAKE + 2) == INVALID and call(idx=FAKE + 4) == INVALID and call(w=FAKE + 2) == INVALID
@@ -55,6 +56,7 @@ def test_router_backward(lib):
     assert call(g=None) == INVALID and call(z=None) == INVALID and call(idx=None) == INVALID
     assert call(out=None) == INVALID and call(out=FAKE + 1) == INVALID and call(idx=FAKE + 4) == INVALID
     assert call(g=FAKE + 2) == INVALID
+    assert call(T=1 << 26, E=257, rs=257) == UNSUPPORTED
     assert call(T=0, g=None, z=None, idx=None, out=None) == 0
 
 
