@@ -19,7 +19,8 @@
 // than the keys' error, without being equal bit by bit in what they are made of,
 // is ordered again, about one of a hundred: the experts taken and the one left
 // that is near them by their values in 64 bits, a lane each; or, where more than
-// one is near or groups are, all of them, by the whole wave.
+// one is near, one that equals the last taken is left or groups are near, all of
+// them, by the whole wave.
 //
 // Backward, one launch: the chosen experts' derivatives are laid into a row of
 // zeros in LDS, from where the row is written in whole vectors; softmax
@@ -491,6 +492,7 @@ __global__ __launch_bounds__(kWaves* kWave) void router_kernel(RouterArgs a) {
             const int from = row * L + a.K - 1;
             const float z_last = __shfl(ze, from), b_last = __shfl(be, from);
             int found = 0, candidate = -1;  // left, within reach, and not equal to the last
+            bool tied = false;              // something left is equal to the last
             for (int j = 0; rest && j < P; ++j) {
                 if (key[0] <= kNone || (key[0] & ~kCut) < reach) break;
                 if (j == DEPTH) {
@@ -501,6 +503,8 @@ __global__ __launch_bounds__(kWaves* kWave) void router_kernel(RouterArgs a) {
                 if (logit<T>(a, base + o) != z_last || (by_value && a.bias[o] != b_last)) {
                     ++found;
                     candidate = o;
+                } else {
+                    tied = true;
                 }
 #pragma unroll
                 for (int i = 0; i + 1 < P; ++i) key[i] = key[i + 1];
@@ -508,8 +512,12 @@ __global__ __launch_bounds__(kWaves* kWave) void router_kernel(RouterArgs a) {
             }
             const uint64_t mine_only = row_lanes(row);
             const uint64_t with = __ballot(found > 0) & mine_only;
-            const bool many = (__ballot(found > 1) & mine_only) != 0 || (with & (with - 1)) != 0;
-            again = (__ballot(again || found > 0) & mine_only) != 0;  // of the row
+            bool many = (__ballot(found > 1) & mine_only) != 0 || (with & (with - 1)) != 0;
+            again = (__ballot(again) & mine_only) != 0;  // of the row: two of the taken may be in the other order
+            // What equals the last expert taken, at a higher index, comes after it, so with the taken in their
+            // order it stays out.  Where one of them may belong behind the last, it may take that one's place.
+            many = many || (again && (__ballot(tied) & mine_only) != 0);
+            again = again || with != 0;
             near = near || (many && again) || (with != 0 && a.K == 16);
             if (__ballot(again && !near) != 0) {
                 // the candidate is one more, in lane K
