@@ -332,7 +332,14 @@ __global__ __launch_bounds__(kWaves* kWave) void router_kernel(RouterArgs a) {
     uint64_t taken = ~0ull;  // the row's groups, a bit each
 
     if (a.groups > 1) {
-        float kept = INFINITY, left = -INFINITY;  // the worst group taken, the best left
+        // How far a group's score may be off for the roundings of its values, of their
+        // sum and of what is made of it below: 4 of 2^-24 of |b1| + |b2|, which may be far
+        // more than the sum (two large biases that cancel); with a margin of two.
+        auto rounding = [&](float b1, float b2) {
+            return 0x1p-21f * fabsf(b1) + (a.top2 ? 0x1p-21f * fabsf(b2) : 0.0f);
+        };
+        // the least that a group taken may be worth, the most that one left may be
+        float kept = INFINITY, left = -INFINITY;
         const int n = a.lanes_per_group;
         if (a.whole_lanes) {
             float b1 = -INFINITY, b2 = -INFINITY;
@@ -364,9 +371,9 @@ __global__ __launch_bounds__(kWaves* kWave) void router_kernel(RouterArgs a) {
                 rank += o > mine || (o == mine && h < g);
             }
             open = g < a.groups && rank < a.topk_groups;
-            if (open) kept = mine;
-            else if (g < a.groups)
-                left = mine;
+            if (open) kept = mine - rounding(b1, b2);
+            else if (g < a.groups && mine > -INFINITY)
+                left = mine + rounding(b1, b2);
         } else {
             float* value = reinterpret_cast<float*>(m.value) + row * a.E;
 #pragma unroll
@@ -389,7 +396,12 @@ __global__ __launch_bounds__(kWaves* kWave) void router_kernel(RouterArgs a) {
                     b2 = fmaxf(fmaxf(b2, o2), fminf(b1, o1));
                     b1 = fmaxf(b1, o1);
                 }
-                if (g < a.groups && part == 0) m.best[row][g] = a.top2 ? b1 + b2 : b1;
+                // place g is one of a group up to g, and those have been read
+                lds_handoff();
+                if (g < a.groups && part == 0) {
+                    m.best[row][g] = a.top2 ? b1 + b2 : b1;
+                    value[g] = rounding(b1, b2);
+                }
                 if (n > 1) break;  // then the lanes cover the groups at once
             }
             lds_handoff();
@@ -406,9 +418,9 @@ __global__ __launch_bounds__(kWaves* kWave) void router_kernel(RouterArgs a) {
                         rank += o > mine || (o == mine && h < g);
                     }
                     in = rank < a.topk_groups;
-                    if (in) kept = fminf(kept, mine);
-                    else
-                        left = fmaxf(left, mine);
+                    if (in) kept = fminf(kept, mine - value[g]);
+                    else if (mine > -INFINITY)
+                        left = fmaxf(left, mine + value[g]);
                 }
                 taken |= ((__ballot(in) >> (row * L)) & (L == kWave ? ~0ull : (1ull << L) - 1)) << (i * L % kWave);
             }
@@ -416,9 +428,8 @@ __global__ __launch_bounds__(kWaves* kWave) void router_kernel(RouterArgs a) {
         if (scored) {  // logits are compared as they are
             kept = -group_max_f32<L>(-kept);
             left = group_max_f32<L>(left);
-            // two sums of two values each, not cut to a key
-            uint64_t todo =
-                __ballot(left > -INFINITY && !(kept - left > 0x1p-21f * (fabsf(kept) + fabsf(left)) + 2 * slack));
+            // the errors of four scores
+            uint64_t todo = __ballot(left > -INFINITY && !(kept - left > 2 * slack));
             while (todo != 0) {
                 const int r = __builtin_ctzll(todo) / L;
                 exact_values<T, Q>(a, first + r, m.value, true, lane);

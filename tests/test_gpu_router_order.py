@@ -81,3 +81,22 @@ def test_saturated_scores_with_a_bias_of_few_steps(E, G, kept, K):
         bias = torch.randint(-steps, steps + 1, (E,), generator=g).float() * 1e-3
         for group_score in ("max", "top2"):
             _same_ids(z, K, "sigmoid", bias=bias, num_groups=G, topk_groups=kept, group_score=group_score)
+
+
+@pytest.mark.parametrize("E,G,kept", [(64, 8, 4), (256, 8, 4), (256, 64, 7), (66, 3, 1), (168, 8, 3), (512, 8, 2),
+                                      (1000, 8, 5)])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_groups_whose_two_best_cancel(E, G, kept, score):
+    """One expert of each group lifted and the others pushed down by as much: a group's score is about one, what
+    rounding leaves of its two values goes with the bias."""
+    g = torch.Generator().manual_seed(E)
+    z = 1.3 * torch.randn(12000, E, generator=g)
+    for size in (1e3, 1e4, 1e6, 1e9):
+        bias = torch.full((G, E // G), -size)
+        bias[torch.arange(G), torch.randint(0, E // G, (G,), generator=g)] = size
+        one = bias.clone()
+        one[1:] = 1e-3 * torch.randint(-60, 61, (G - 1, E // G), generator=g)  # in the first group only
+        for b in (bias, one):
+            _log(f"E={E} G={G}/{kept} {score} {size}")
+            _same_ids(z, min(4, kept * (E // G)), score, bias=b.flatten(), num_groups=G, topk_groups=kept,
+                      group_score="top2")
