@@ -658,10 +658,12 @@ moe_status moe_expert_matvec(const void* x, int32_t x_dtype, const float* x_sf, 
  *     descending order;
  *   - topk_weights[t, k] = scale * s[t, topk_idx[t, k]], with renormalize = 1
  *     divided by the sum of the K scores.  The bias has no part in them.
- * Equal values go to the lowest index.  Values are ordered as 64-bit numbers
- * hold them, with no bias and MOE_GROUP_MAX as the logits themselves are;
- * weights are computed in fp32, renormalised ones without underflow whatever
- * the logits.
+ * Equal values go to the lowest index.  What is ordered: with a bias, c in
+ * 64-bit numbers; without one the logits themselves, whatever their scores
+ * round to, except that MOE_GROUP_TOP2 judges groups by 64-bit scores always.
+ * (Sums that are equal as real numbers may differ by a 64-bit rounding, and
+ * then come in that order.)  Weights are computed in fp32, renormalised ones
+ * without underflow whatever the logits.
  *
  * An expert whose logit is -inf or NaN, or whose bias is -inf or NaN, is not
  * taken; a logit or bias of +inf counts as the largest finite number.  Where

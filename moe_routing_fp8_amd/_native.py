@@ -1094,9 +1094,9 @@ def moe_router(logits: torch.Tensor, num_topk: int, score: str = "softmax", bias
     largest score + bias among the `topk_groups` best of `num_groups` groups, in descending order, and their scores
     times `scale` (`renormalize`: divided by their sum) -> (topk_idx int64 [T, K], topk_weights fp32 [T, K]).
     `score`: "softmax" or "sigmoid"; bias fp32 [E]; `group_score`: a group's best score + bias ("max") or the sum of
-    its two best ("top2").  token_mask bool [T]: a token that is False gets ids -1 and weights 0, as does a round for
-    which no expert is left (logits of -inf or NaN are none).  Nothing is recorded for autograd: the gradient comes
-    from moe_router_backward."""
+    its two best ("top2"); without a bias experts are ordered by their logits.  token_mask bool [T]: a token that is
+    False gets ids -1 and weights 0, as does a round for which no expert is left (logits of -inf or NaN are none).
+    Nothing is recorded for autograd: the gradient comes from moe_router_backward."""
     stride, mode, _ = _balance_inputs(logits, score, token_mask, None)
     T, E = logits.shape
     dev = logits.device

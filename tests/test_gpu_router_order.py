@@ -100,3 +100,21 @@ def test_groups_whose_two_best_cancel(E, G, kept, score):
             _log(f"E={E} G={G}/{kept} {score} {size}")
             _same_ids(z, min(4, kept * (E // G)), score, bias=b.flatten(), num_groups=G, topk_groups=kept,
                       group_score="top2")
+
+
+@pytest.mark.parametrize("E", [16, 66, 256, 320])
+def test_saturated_logits_without_a_bias(E):
+    """Sigmoids that are 1 in 64 bits: experts come by their logits, with groups too; groups judged by their two best are
+    equal then and go to the lowest, those judged by their best go by its logit."""
+    G, size = 2, E // 2
+    z = torch.full((2, E), 40.0)
+    z[:, size - 1], z[:, 3] = 42.0, 41.0
+    z[1, E - 1] = 43.0
+    kw = dict(score="sigmoid", num_groups=G, topk_groups=1)
+    idx, _ = moe.moe_router(z.cuda(), 3, group_score="top2", **kw)
+    assert idx.tolist() == [[size - 1, 3, 0], [size - 1, 3, 0]]
+    idx, _ = moe.moe_router(z.cuda(), 3, group_score="max", **kw)
+    assert idx.tolist() == [[size - 1, 3, 0], [E - 1, size, size + 1]]
+    # with a bias, one of zeros too, equal scores go to the lowest expert
+    idx, _ = moe.moe_router(z.cuda(), 3, group_score="top2", bias=torch.zeros(E, device="cuda"), **kw)
+    assert idx.tolist() == [[0, 1, 2]] * 2
