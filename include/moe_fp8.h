@@ -748,7 +748,8 @@ moe_status swiglu_cast_int8(const uint16_t* gate_up_bf16, int64_t num_rows, int3
                             float clamp_value, int8_t* out, float* out_sf, hipStream_t stream);
 
 #define MOE_MATMUL_INT8_MAX_INNER 131071 /* 2^31 over the largest product of two codes, 2^14 */
-#define MOE_MATMUL_INT8_MAX_TILES 16777216 /* of 16 rows and 64 channels: a launch's workgroups */
+#define MOE_MATMUL_INT8_ANY_WIDTH_ROWS 67108864 /* rows up to which any out_width is taken */
+#define MOE_MATMUL_INT8_MAX_TILES 16777216 /* of 16 rows and 64 channels, with more rows: a limit on a call's size */
 
 /*
  * moe_expert_matmul_int8 -- the experts' products in 8-bit integers: rows
@@ -767,7 +768,8 @@ moe_status swiglu_cast_int8(const uint16_t* gate_up_bf16, int64_t num_rows, int3
  *                num_rows is 0).
  * num_rows       R >= 0.
  * inner          1 <= inner <= MOE_MATMUL_INT8_MAX_INNER, out_width N <=
- *                MOE_MATVEC_MAX_WIDTH, (R / 16 + E) * ceil(N / 64) below
+ *                MOE_MATVEC_MAX_WIDTH; with R of MOE_MATMUL_INT8_ANY_WIDTH_ROWS
+ *                or more, (R / 16 + E) * ceil(N / 64) below
  *                MOE_MATMUL_INT8_MAX_TILES (else: MOE_ERR_UNSUPPORTED).
  * num_experts    E, 1 <= E <= 1024.
  * expert_offsets int32 [E + 1], non-decreasing, within [0, R] (from

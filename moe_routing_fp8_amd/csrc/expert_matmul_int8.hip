@@ -694,7 +694,11 @@ extern "C" moe_status moe_expert_matmul_int8(const int8_t* x, const float* x_sf,
     if (expert_offsets == nullptr && num_experts != 1) return MOE_ERR_INVALID_ARGUMENT;
     // beyond it a sum of products of codes could leave 32 bits
     if (inner > MOE_MATMUL_INT8_MAX_INNER || out_width > MOE_MATVEC_MAX_WIDTH) return MOE_ERR_UNSUPPORTED;
-    if ((num_rows / kMinRows + num_experts) * ((out_width + kMinChannels - 1) / kMinChannels) >= MOE_MATMUL_INT8_MAX_TILES)
+    // the sums over the experts' row tiles and their costs, 32 bits, and the rows' rounding up to whole tiles hold for
+    // fewer than 2^28 rows, which the second condition leaves; tiles are numbered in 64 bits
+    if (num_rows >= MOE_MATMUL_INT8_ANY_WIDTH_ROWS &&
+        (num_rows / kMinRows + num_experts) * ((out_width + kMinChannels - 1) / kMinChannels) >=
+            MOE_MATMUL_INT8_MAX_TILES)
         return MOE_ERR_UNSUPPORTED;
     if (num_rows == 0) return MOE_OK;  // an empty row_token may be null: x_rows is then anything
     if (row_token == nullptr && x_rows != num_rows) return MOE_ERR_INVALID_ARGUMENT;
