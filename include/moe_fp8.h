@@ -38,7 +38,7 @@
  *   of such rows with 8-bit weights, from one row to a prompt's.
  *
  * Device-side checks of the inputs' preconditions, for debugging:
- *   moe_check_scores, moe_check_topk_idx, moe_check_pos,
+ *   moe_check_scores, moe_check_topk_idx, moe_check_routed_idx, moe_check_pos,
  *   moe_check_activations, and of a single-launch dispatch's barrier:
  *   moe_check_dispatch
  *
@@ -959,6 +959,9 @@ moe_status moe_dispatch(const float* scores, const uint16_t* x_bf16, int64_t num
  * moe_check_topk_idx topk_idx int64 [T, K] (8-byte aligned): every id in
  *   [0, E) and no id twice in a row ([TK] 2.1: each round masks its
  *   winner, so a token's K ids are distinct experts).  K <= 16, E <= 1024.
+ * moe_check_routed_idx   the same of ids that moe_router wrote: an id of -1 is
+ *   a copy without an expert (a masked token's, or a round's for which none
+ *   was left), which moe_token_map leaves out; any number of them.
  * moe_check_pos      pos int32 [T, K] (4-byte aligned): every entry in
  *   [-1, num_rows) and no row reached by two copies ([TK] 2.2: -1 marks a
  *   skipped copy; every other copy owns its destination row).  workspace:
@@ -967,7 +970,7 @@ moe_status moe_dispatch(const float* scores, const uint16_t* x_bf16, int64_t num
  */
 #define MOE_CHECK_NONFINITE_SCORE 0x01u   /* a score is NaN or infinite */
 #define MOE_CHECK_NONPOSITIVE_SCORE 0x02u /* require_positive and a finite score <= 0 */
-#define MOE_CHECK_ID_RANGE 0x04u          /* an id outside [0, E) */
+#define MOE_CHECK_ID_RANGE 0x04u          /* an id outside [0, E), or for routed ids [-1, E) */
 #define MOE_CHECK_ID_DUPLICATE 0x08u      /* an id repeated within a token's row */
 #define MOE_CHECK_POS_RANGE 0x10u         /* an entry outside [-1, num_rows) */
 #define MOE_CHECK_POS_DUPLICATE 0x20u     /* two copies with the same destination row */
@@ -978,6 +981,8 @@ moe_status moe_check_scores(const float* scores, int64_t num_tokens, int32_t num
                             int32_t require_positive, uint32_t* flags, hipStream_t stream);
 moe_status moe_check_topk_idx(const int64_t* topk_idx, int64_t num_tokens, int32_t num_topk,
                               int32_t num_experts, uint32_t* flags, hipStream_t stream);
+moe_status moe_check_routed_idx(const int64_t* topk_idx, int64_t num_tokens, int32_t num_topk,
+                                int32_t num_experts, uint32_t* flags, hipStream_t stream);
 /* Bytes of workspace moe_check_pos needs: 4 * ceil(num_rows / 32) (0 for
  * num_rows <= 0). */
 size_t moe_check_pos_workspace_bytes(int64_t num_rows);

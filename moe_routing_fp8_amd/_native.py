@@ -82,6 +82,7 @@ _SIGNATURES = {
     "moe_expert_matmul_int8": ([_p, _p, _i64, _p, _i64, _i32, _i32, _i32, _p, _p, _p, _i32, _p, _p], ctypes.c_int),
     "moe_check_scores": ([_p, _i64, _i32, _i32, _p, _p], ctypes.c_int),
     "moe_check_topk_idx": ([_p, _i64, _i32, _i32, _p, _p], ctypes.c_int),
+    "moe_check_routed_idx": ([_p, _i64, _i32, _i32, _p, _p], ctypes.c_int),
     "moe_check_pos_workspace_bytes": ([_i64], _sz),
     "moe_check_pos": ([_p, _i64, _i32, _i64, _p, _sz, _p, _p], ctypes.c_int),
     "moe_check_activations": ([_p, _i64, _p, _p], ctypes.c_int),
@@ -266,11 +267,20 @@ def moe_check_scores(scores: torch.Tensor, require_positive: bool = False, flags
 
 def moe_check_topk_idx(topk_idx: torch.Tensor, num_experts: int, flags=None, stream=None) -> torch.Tensor:
     """ORs MOE_CHECK_ID_RANGE / MOE_CHECK_ID_DUPLICATE into `flags` for the int64 [T, K] ids."""
+    return _check_ids("moe_check_topk_idx", topk_idx, num_experts, flags, stream)
+
+
+def moe_check_routed_idx(topk_idx: torch.Tensor, num_experts: int, flags=None, stream=None) -> torch.Tensor:
+    """moe_check_topk_idx for ids as moe_router writes them: any number of -1, copies without an expert."""
+    return _check_ids("moe_check_routed_idx", topk_idx, num_experts, flags, stream)
+
+
+def _check_ids(name, topk_idx, num_experts, flags, stream):
     _need(topk_idx, torch.int64, 2, "topk_idx")
     T, K = topk_idx.shape
     dev = topk_idx.device
     flags = _flags(flags, dev, stream)
-    _call("moe_check_topk_idx", dev, stream, _ptr(topk_idx), T, K, num_experts, _ptr(flags))
+    _call(name, dev, stream, _ptr(topk_idx), T, K, num_experts, _ptr(flags))
     return flags
 
 
@@ -391,7 +401,7 @@ def moe_token_map(topk_idx: torch.Tensor, num_experts: int, with_row_token: bool
         with _alloc_on(stream):
             workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
     if debug_enabled():
-        _debug_raise("moe_token_map", lambda: moe_check_topk_idx(topk_idx, num_experts, stream=stream), stream)
+        _debug_raise("moe_token_map", lambda: moe_check_routed_idx(topk_idx, num_experts, stream=stream), stream)
     _call("moe_token_map", dev, stream, _ptr(topk_idx), T, K, num_experts, _ptr(counts), _ptr(offsets), _ptr(pos),
           _ptr(row_token), _ptr(workspace), _workspace(workspace, dev))
     return counts, offsets, pos, row_token
@@ -417,7 +427,7 @@ def moe_token_map_noalloc(topk_idx: torch.Tensor, num_experts: int, with_row_tok
         _need_out(pos, torch.int32, (T, K), "pos", dev)
         _need_out(row_token, torch.int32, (T * K,), "row_token", dev)
     if debug_enabled():
-        _debug_raise("moe_token_map_noalloc", lambda: moe_check_topk_idx(topk_idx, num_experts, stream=stream),
+        _debug_raise("moe_token_map_noalloc", lambda: moe_check_routed_idx(topk_idx, num_experts, stream=stream),
                      stream)
     _call("moe_token_map_noalloc", dev, stream, _ptr(topk_idx), T, K, num_experts, _ptr(counts), _ptr(offsets),
           _ptr(pos), _ptr(row_token))

@@ -7,7 +7,8 @@
 //               divided by the sum of the selected scores);
 //   topk_idx    every id in [0, E) and no id twice in one token's row
 //               (section 2.1: each round masks its winner, so a row's K ids
-//               are K distinct experts);
+//               are K distinct experts); of routed ids, -1 is none and may
+//               repeat;
 //   pos         every entry in [-1, num_rows) and no row reached by two
 //               copies (section 2.2: -1 marks a copy that is skipped; every
 //               other copy owns its destination row);
@@ -52,7 +53,7 @@ __global__ __launch_bounds__(kCheckThreads) void check_scores_kernel(const float
 // One thread per token row: K <= 16 ids, pairwise compared.
 __global__ __launch_bounds__(kCheckThreads) void check_topk_idx_kernel(const int64_t* __restrict__ idx,
                                                                        int64_t num_tokens, int num_topk,
-                                                                       int num_experts,
+                                                                       int num_experts, bool allow_none,
                                                                        uint32_t* __restrict__ flags) {
     uint32_t bits = 0;
     const int64_t stride = static_cast<int64_t>(gridDim.x) * kCheckThreads;
@@ -60,6 +61,7 @@ __global__ __launch_bounds__(kCheckThreads) void check_topk_idx_kernel(const int
         const int64_t* row = idx + t * num_topk;
         for (int k = 0; k < num_topk; ++k) {
             const int64_t e = row[k];
+            if (allow_none && e == -1) continue;
             if (e < 0 || e >= num_experts) bits |= MOE_CHECK_ID_RANGE;
             for (int j = 0; j < k; ++j)
                 if (row[j] == e) bits |= MOE_CHECK_ID_DUPLICATE;
@@ -127,9 +129,9 @@ hipError_t launch_check_scores(const float* scores, int64_t num_tokens, int num_
 }
 
 hipError_t launch_check_topk_idx(const int64_t* idx, int64_t num_tokens, int num_topk, int num_experts,
-                                 uint32_t* flags, hipStream_t stream) {
+                                 bool allow_none, uint32_t* flags, hipStream_t stream) {
     hipLaunchKernelGGL(check_topk_idx_kernel, dim3(check_blocks(num_tokens)), dim3(kCheckThreads), 0, stream, idx,
-                       num_tokens, num_topk, num_experts, flags);
+                       num_tokens, num_topk, num_experts, allow_none, flags);
     return hipGetLastError();
 }
 

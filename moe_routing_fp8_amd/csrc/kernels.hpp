@@ -117,7 +117,7 @@ hipError_t launch_dispatch_fused(const float* scores, const uint16_t* x, int64_t
 hipError_t launch_check_scores(const float* scores, int64_t num_tokens, int num_experts, bool require_positive,
                                uint32_t* flags, hipStream_t stream);
 hipError_t launch_check_topk_idx(const int64_t* topk_idx, int64_t num_tokens, int num_topk, int num_experts,
-                                 uint32_t* flags, hipStream_t stream);
+                                 bool allow_none, uint32_t* flags, hipStream_t stream);
 hipError_t launch_check_pos(const int32_t* pos, int64_t num_entries, int64_t num_rows, uint32_t* seen,
                             uint32_t* flags, hipStream_t stream);
 hipError_t launch_check_bf16(const uint16_t* x, int64_t n, uint32_t* flags, hipStream_t stream);

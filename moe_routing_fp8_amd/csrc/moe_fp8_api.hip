@@ -496,15 +496,25 @@ moe_status moe_check_scores(const float* scores, int64_t num_tokens, int32_t num
                                                stream));
 }
 
-moe_status moe_check_topk_idx(const int64_t* topk_idx, int64_t num_tokens, int32_t num_topk,
-                              int32_t num_experts, uint32_t* flags, hipStream_t stream) {
+static moe_status check_ids(const int64_t* topk_idx, int64_t num_tokens, int32_t num_topk, int32_t num_experts,
+                            bool allow_none, uint32_t* flags, hipStream_t stream) {
     if (num_tokens < 0 || num_topk < 1 || num_topk > kMaxTopk) return MOE_ERR_INVALID_ARGUMENT;
     if (num_experts < 1 || num_experts > kMaxExperts) return MOE_ERR_INVALID_ARGUMENT;
     if (num_tokens > INT64_MAX / kMaxTopk) return MOE_ERR_INVALID_ARGUMENT;
     if (flags == nullptr || !aligned(flags, 4)) return MOE_ERR_INVALID_ARGUMENT;
     if (num_tokens == 0) return MOE_OK;
     if (topk_idx == nullptr || !aligned(topk_idx, 8)) return MOE_ERR_INVALID_ARGUMENT;
-    return hip_status(moe::launch_check_topk_idx(topk_idx, num_tokens, num_topk, num_experts, flags, stream));
+    return hip_status(moe::launch_check_topk_idx(topk_idx, num_tokens, num_topk, num_experts, allow_none, flags, stream));
+}
+
+moe_status moe_check_topk_idx(const int64_t* topk_idx, int64_t num_tokens, int32_t num_topk,
+                              int32_t num_experts, uint32_t* flags, hipStream_t stream) {
+    return check_ids(topk_idx, num_tokens, num_topk, num_experts, false, flags, stream);
+}
+
+moe_status moe_check_routed_idx(const int64_t* topk_idx, int64_t num_tokens, int32_t num_topk,
+                                int32_t num_experts, uint32_t* flags, hipStream_t stream) {
+    return check_ids(topk_idx, num_tokens, num_topk, num_experts, true, flags, stream);
 }
 
 size_t moe_check_pos_workspace_bytes(int64_t num_rows) {
