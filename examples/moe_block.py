@@ -82,10 +82,12 @@ class Block:
                                       renormalize=True, token_mask=token_mask)
         _, offsets, pos, row_token = moe.moe_token_map(ids, self.experts)
         codes, sf = moe.moe_cast_int8(x)
-        up = torch.zeros(row_token.numel(), self.up_int8[0].shape[1], dtype=torch.bfloat16, device=x.device)
+        # the rows behind the last expert's, of masked tokens, stay zeros
+        up, down = (torch.zeros(row_token.numel(), w[0].shape[1], dtype=torch.bfloat16, device=x.device)
+                    for w in (self.up_int8, self.down_int8))
         moe.moe_expert_matmul_int8(codes, sf, *self.up_int8, expert_offsets=offsets, row_token=row_token, out=up)
-        act, act_sf = moe.swiglu_cast_int8(up)  # the rows behind the last expert's are zeros
-        down = moe.moe_expert_matmul_int8(act, act_sf, *self.down_int8, expert_offsets=offsets)
+        act, act_sf = moe.swiglu_cast_int8(up)
+        moe.moe_expert_matmul_int8(act, act_sf, *self.down_int8, expert_offsets=offsets, out=down)
         y = moe.moe_combine(down, pos, weights)
         out, normed, _, _ = moe.moe_block_norm(residual, y, post_weight=self.norm_after, gate=self.gate,
                                                pre_weight=self.norm_next)
