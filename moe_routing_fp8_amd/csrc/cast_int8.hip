@@ -9,7 +9,8 @@
 // 512 channels) or a workgroup holds the row in registers, 8 channels a lane
 // and step, so it is read once; wider rows than kMaxSteps steps of a workgroup
 // are read again.  Bound by bytes and, at these sizes, by start and drain: 2048 x
-// 7168 bf16 take 11.7 us (3.8 TB/s), SwiGLU of 4096 x 2 x 2048 10.3 us (4.1 TB/s).
+// 7168 bf16 take 12.1 us (3.6 TB/s), SwiGLU of 4096 x 2 x 2048 10.8 us (3.9 TB/s;
+// medians of kernel traces).
 #include <hip/hip_runtime.h>
 
 #include "api_common.hpp"

@@ -10,9 +10,9 @@
 // there.
 //
 // 32 experts, 7168 -> 4096, bf16 out (back to back, rotating inputs):
-//   128 rows             96 to 108 us    bytes of the weights, part of them in the last-level cache
-//   4096 rows by token   246 to 288 us   loads into LDS, and 2.1 to 3.0 tiles a compute unit
-//   16384 rows by token  587 to 621 us   1.55 to 1.64 POPS: loads into LDS, unequal experts
+//   128 rows             96 to 108 us    bytes of the weights: 20 experts have rows, 5.5 to 6.2 TB/s
+//   4096 rows by token   246 to 288 us   loads into LDS, waits at the tiles' ends, 2.1 to 3.0 tiles a compute unit
+//   16384 rows by token  587 to 621 us   1.55 to 1.64 POPS: the same, unequal experts
 // One matrix, 16384 rows, 8192 -> 8192: 943 to 985 us, 2.2 to 2.3 POPS.  Multiplying
 // alone takes 74% of that, loading alone 79%; random codes in registers reach 4.1 POPS.
 #include <hip/hip_runtime.h>
@@ -330,10 +330,14 @@ __device__ __forceinline__ void load4_to_lds(const void* p, uint32_t lds) {
 
 // Rows of whole, aligned 16-byte chunks.  The workgroup stays and takes one tile
 // after another; its loads run ahead of the products, SX - 1 steps those of x and
-// SW - 1 those of w, across the tiles' ends, so that neither the start of a tile
-// nor its stores leave the matrix units or the memory idle.  A tile's scales are
-// loaded with its first steps.  SX is SW, or 2 where LDS has no room for more: x
-// comes from the L2 mostly, w from memory.
+// SW - 1 those of w, across the tiles' ends.  A tile's scales are loaded with its
+// first steps.  SX is SW, or 2 where LDS has no room for more: x comes from the L2
+// mostly, w from memory.
+//
+// A tile's border is not free: the compiler does not know of the loads into LDS and
+// waits for everything under way where it uses the tile's row tokens, and before it
+// writes their registers again; the tile's stores count in the first wait_loads
+// behind them.  Up to three such waits a tile, of 16 steps with 2048 of k.
 template <int BM, int BN, int BK, int SX, int SW, int WM, int WN>
 __global__ __launch_bounds__(WM* WN* kWave) void expert_matmul_int8_kernel(MatmulArgs a) {
     using Y = Layout<BM, BN, BK, WM, WN>;

@@ -26,12 +26,16 @@
 // zeros in LDS, from where the row is written in whole vectors; softmax
 // weights without renormalisation add the term of every other expert.
 //
-// Kernel traces:
-//   32768 x 256 fp32, sigmoid, bias, 4 of 8 groups    19.6 us (7.2 of bytes): about 1000 vector
-//                                                     instructions a wave of four rows
-//   32768 x 256 bf16, softmax; its whole gradient     14.1 + 8.1 us (3.3 and 6.6 of bytes)
-//   10007 x 61 fp32, softmax, bias; its gradient      6.7 + 3.6 us
-//   1 x 256 fp32, sigmoid, bias, groups               4.5 us, latency
+// Kernel traces, the chip idle before each call, median (least) of 20:
+//   32768 x 256 fp32, sigmoid, bias, 4 of 8 groups    25.2 (19.8) us (7.2 of bytes), back to back 19.7:
+//                                                     about 1000 vector instructions a wave of four
+//                                                     rows, part of them for groups already refused
+//   32768 x 256 bf16, softmax; its whole gradient     14.9 (14.6) + 9.1 (8.2) us (3.3 and 6.6 of bytes)
+//   10007 x 61 fp32, softmax, bias; its gradient      7.0 (6.5) + 3.9 (3.6) us
+//   1 x 256 fp32, sigmoid, bias, groups               4.7 (4.6) us: two trips to memory, the logits and,
+//                                                     once ranked, the chosen ones again
+// Where every row has to be ordered again, back to back: 32768 x 256 bf16 sigmoids around
+// 8 with a bias of zeros 87 us, all logits 0 in 8 groups judged by their two best 141 us.
 // Sixteen lanes a row: a round's maximum takes four DPP steps for four rows; with
 // a row over all 64 lanes, as many steps and more for each.
 #include <hip/hip_runtime.h>
