@@ -109,6 +109,11 @@ struct Tiles {
             mine += n;
             weight += n * tile_cost(tile_rows(count, n));
         }
+        // Offsets that decrease can give many experts the same rows.  Up to 2^30 of cost they
+        // are computed all the same; beyond that, where the sums would leave 32 bits (a lane's
+        // own, of at most 16 experts of 2^28 rows, does not), there are no tiles.
+        if (__builtin_amdgcn_readlane(wave_scan(weight / kWave, lane), kWave - 1) >= (1 << 30) / kWave)
+            mine = weight = 0;
         tiles_to = wave_scan(mine, lane);
         cost_to = wave_scan(weight, lane);
         total = __builtin_amdgcn_readlane(tiles_to, kWave - 1);

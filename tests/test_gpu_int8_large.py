@@ -1,4 +1,4 @@
-"""moe_expert_matmul_int8 with many rows and many channels at once."""
+"""moe_expert_matmul_int8 with many rows and many channels at once, and with offsets that give many experts many rows."""
 import pytest
 import torch
 
@@ -28,3 +28,18 @@ def test_many_rows_by_many_channels(K):
         rows = rows.cuda()
         sums = x[rows].double() @ w[e].double().t().contiguous()
         assert torch.equal(y[rows], ((sums.float() * x_sf[rows, None]) * w_sf[e]).to(BF16)), (e, int(rows[0]))
+
+
+@pytest.mark.parametrize("K", [16, 1])
+def test_offsets_that_give_every_second_expert_all_rows(K):
+    """512 experts of nearly 2^26 rows each, which no valid offsets give: nothing is computed, nothing outside is read.
+    (With 2 experts the same rows are computed.)"""
+    R, E = (1 << 26) - 1, 1024
+    x, x_sf = torch.ones(R, K, dtype=I8, device="cuda"), torch.ones(R, device="cuda")
+    w, w_sf = torch.ones(E, 1, K, dtype=I8, device="cuda"), torch.ones(E, 1, device="cuda")
+    out = torch.full((R + 2, 1), 7.0, dtype=BF16, device="cuda")
+    off = torch.tensor([0, R] * (E // 2) + [0], dtype=I32, device="cuda")
+    moe.moe_expert_matmul_int8(x, x_sf, w, w_sf, expert_offsets=off, out=out[1:-1])
+    assert (out == 7).all()
+    moe.moe_expert_matmul_int8(x, x_sf, w[:2], w_sf[:2], expert_offsets=off[:3], out=out[1:-1])
+    assert (out[1:-1] == K).all() and out[0] == 7 and out[-1] == 7
