@@ -748,7 +748,7 @@ moe_status swiglu_cast_int8(const uint16_t* gate_up_bf16, int64_t num_rows, int3
                             float clamp_value, int8_t* out, float* out_sf, hipStream_t stream);
 
 #define MOE_MATMUL_INT8_MAX_INNER 131071 /* 2^31 over the largest product of two codes, 2^14 */
-#define MOE_MATMUL_INT8_ANY_WIDTH_ROWS 67108864 /* rows up to which any out_width is taken */
+#define MOE_MATMUL_INT8_ANY_WIDTH_ROWS 67108864 /* below so many rows any out_width is taken */
 #define MOE_MATMUL_INT8_MAX_TILES 16777216 /* of 16 rows and 64 channels, with more rows: a limit on a call's size */
 
 /*

@@ -504,7 +504,8 @@ static moe_status check_ids(const int64_t* topk_idx, int64_t num_tokens, int32_t
     if (flags == nullptr || !aligned(flags, 4)) return MOE_ERR_INVALID_ARGUMENT;
     if (num_tokens == 0) return MOE_OK;
     if (topk_idx == nullptr || !aligned(topk_idx, 8)) return MOE_ERR_INVALID_ARGUMENT;
-    return hip_status(moe::launch_check_topk_idx(topk_idx, num_tokens, num_topk, num_experts, allow_none, flags, stream));
+    return hip_status(moe::launch_check_topk_idx(topk_idx, num_tokens, num_topk, num_experts, allow_none, flags,
+                                                 stream));
 }
 
 moe_status moe_check_topk_idx(const int64_t* topk_idx, int64_t num_tokens, int32_t num_topk,
